@@ -1,0 +1,100 @@
+/*
+ * ssm_hybrid.h -- C ABI of the operators of a hybrid block: what a stack of
+ * layers needs beside the selective scan of ssm_scan.h when some layers are
+ * gated linear recurrences and some attend over a local window.
+ *
+ *   ssm_glr_*      gated linear recurrence: forward, backward, single token
+ *   ssm_qk_rope_*  norm and rotation of queries and keys: forward, backward,
+ *                  and the append of new tokens to a window cache
+ *   ssm_swa_*      attention with a sliding window and sinks: forward,
+ *                  backward, single tokens over the window cache
+ *
+ * The conventions of ssm_scan.h hold: device pointers, caller-owned buffers,
+ * arguments checked on the host before any HIP call, kernels enqueued on
+ * `stream`, ssm_status results, dtype (ssm_dtype) for the tensors said to be
+ * "of dtype", float32 sums and states, every pointer aligned to 16 bytes,
+ * results that do not depend on timing (repeated calls give identical bits).
+ * Empty inputs are valid, and a buffer with no elements may then be NULL.
+ *
+ * Strides. The q, k and v arguments of ssm_qk_rope_* and ssm_swa_* (and
+ * nothing else) may lie in a larger tensor, such as the packed output of one
+ * projection: ssm_strides gives the distance, in elements, from one batch
+ * row, token and head to the next; the D entries of a head are contiguous.
+ * NULL means dense row-major. Strides are not negative (zero repeats the
+ * same data) and are multiples of 16 bytes, else SSM_ERR_UNSUPPORTED.
+ */
+#ifndef SSM_HYBRID_H
+#define SSM_HYBRID_H
+
+#include "ssm_scan.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef struct {
+  int64_t batch, token, head; /* elements */
+} ssm_strides;
+
+/*
+ * Gated linear recurrence. One state per channel; the gates come as logits.
+ * For batch row b and channel e, with h_{-1} = h0 (zero if NULL):
+ *
+ *   r = sigmoid(gr[b,t,e]),  i = sigmoid(gi[b,t,e]),  la = A[e] r
+ *   h_t = exp(la) h_{t-1} + sqrt(max(0, 1 - exp(2 la))) i x[b,t,e]
+ *   y[b,t,e] = h_t
+ *
+ * A is the log decay of a fully open gate, negative (as A of the selective
+ * scan); the square root keeps the size of the state independent of the
+ * decay. 1 - exp(2 la) is formed without cancellation near la = 0. A channel
+ * with A >= 0 takes no input (the root is zero) and decays by exp(la) >= 1.
+ *   x, gr, gi : (Bs, L, ED) of dtype
+ *   A         : (ED) float32
+ *   h0        : (Bs, ED) float32, or NULL
+ *   y         : (Bs, L, ED) of dtype, written in full
+ *   h_last    : (Bs, ED) float32, or NULL -- the state after the last step
+ *   ckpt      : float32, or NULL -- the state entering every
+ *               SSM_GLR_CKPT_STEPS steps, (Bs, ceil(L / SSM_GLR_CKPT_STEPS),
+ *               ED), for ssm_glr_bwd; ssm_glr_ckpt_bytes() bytes
+ *   workspace : ssm_glr_workspace_bytes() bytes; no initialisation needed.
+ *               NULL when that is zero
+ */
+#define SSM_GLR_CKPT_STEPS 16
+size_t ssm_glr_ckpt_bytes(int64_t Bs, int64_t L, int64_t ED);
+size_t ssm_glr_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype);
+int ssm_glr_fwd(const void* x, const void* gr, const void* gi, const float* A, const float* h0, void* y,
+                float* h_last, float* ckpt, int64_t Bs, int64_t L, int64_t ED, int dtype, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass: the gradients of sum(dy y) + sum(dh_last h_last). With the
+ * adjoint g_t = dy_t + exp(la_{t+1}) g_{t+1} (dh_last added at the last step),
+ * a = exp(la) and s the square root above:
+ *   dx  = g s i                    dgi = g s x i (1 - i)
+ *   dla = g (a h_{t-1} - (a^2 / s) i x)      (second term 0 where s = 0)
+ *   dgr = dla A r (1 - r)          dA  = sum_{b,t} dla r        dh0 = a_0 g_0
+ *   ckpt    : the states that ssm_glr_fwd wrote for the same inputs (those
+ *             of other inputs give wrong gradients, no error); it holds h0
+ *   dy      : (Bs, L, ED) of dtype;  dh_last : (Bs, ED) float32, or NULL
+ *   dx, dgr, dgi : (Bs, L, ED) of dtype;  dA : (ED) float32
+ *   dh0     : (Bs, ED) float32, or NULL (not computed)
+ *   workspace : ssm_glr_bwd_workspace_bytes() bytes, no initialisation needed
+ */
+size_t ssm_glr_bwd_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype);
+int ssm_glr_bwd(const void* x, const void* gr, const void* gi, const float* A, const float* ckpt, const void* dy,
+                const float* dh_last, void* dx, void* dgr, void* dgi, float* dA, float* dh0, int64_t Bs, int64_t L,
+                int64_t ED, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token: x, gr, gi and y are (Bs, ED) of dtype; the state goes from h to
+ * h_out ((Bs, ED) float32; h_out may be h itself, and overlaps it in no
+ * other way).
+ */
+int ssm_glr_step(const void* x, const void* gr, const void* gi, const float* A, const float* h, void* y,
+                 float* h_out, int64_t Bs, int64_t ED, int dtype, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSM_HYBRID_H */

@@ -3,18 +3,24 @@
 Argument marshalling only: every step of the scan runs in the HIP kernels of
 ``csrc/ssm_scan.hip`` (forward), ``csrc/ssm_scan_bwd.hip`` (backward) and
 ``csrc/ssm_ssd.hip`` (multi-head scan) behind the C ABI declared in
-``include/ssm_scan.h``.
+``include/ssm_scan.h``. The operators of a hybrid block (``hybrid.py``) are
+part of the same library, declared in ``include/ssm_hybrid.h``.
 PyTorch supplies device memory and the stream. There is no fallback: if the
 library is not built, or the tensors are not on a GPU, the calls raise.
 """
+import concurrent.futures
 import ctypes
 import os
 import subprocess
 
+from .hybrid import (PROTOTYPES as _HYBRID_PROTOTYPES, ssm_glr_bwd, ssm_glr_bwd_workspace_bytes, ssm_glr_ckpt_shape,
+                     ssm_glr_fwd, ssm_glr_step, ssm_glr_workspace_bytes)
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libssm_scan.so")
-SOURCES = [os.path.join(_HERE, "csrc", n) for n in ("ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_ssd.hip")]
+SOURCES = [os.path.join(_HERE, "csrc", n) for n in ("ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_ssd.hip",
+                                                    "ssm_glr.hip")]
 # issue-rate probe of the vector ALU (measurement only; used by the benchmark's --micro mode)
 PROBE_LIB_PATH = os.path.join(_HERE, "libssm_valu_probe.so")
 PROBE_SOURCES = [os.path.join(_HERE, "csrc", "valu_probe.hip")]
@@ -33,7 +39,7 @@ class SSMOptions(ctypes.Structure):
                 ("dt_max", ctypes.c_float), ("z", ctypes.c_void_p)]
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", "-fPIC", "-shared", "--offload-arch=gfx950",
+    "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950",
     # no packed-FP32 instructions anywhere in the library
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
@@ -49,16 +55,31 @@ class SSMError(RuntimeError):
         super().__init__("%s: %s (status %d)" % (where, status_str(status), status))
 
 
-def _hipcc(sources, out, verbose):
+def _run_hipcc(args, verbose):
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = out + ".tmp"
-    cmd = [hipcc] + HIPCC_FLAGS + ["-I", INCLUDE] + sources + ["-o", tmp]
-    res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    res = subprocess.run([hipcc] + HIPCC_FLAGS + args, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + res.stdout)
     if verbose:
         print(res.stdout)
-    os.replace(tmp, out)
+
+
+def _hipcc(sources, out, verbose):
+    """Compiles the sources side by side (at most eight at once), then links them."""
+    tmp = out + ".tmp"
+    objects = ["%s.%d.o" % (tmp, i) for i in range(len(sources))]
+    try:
+        with concurrent.futures.ThreadPoolExecutor(min(8, len(sources))) as pool:
+            jobs = [pool.submit(_run_hipcc, ["-I", INCLUDE, "-c", s, "-o", o], verbose)
+                    for s, o in zip(sources, objects)]
+            for j in jobs:
+                j.result()
+        _run_hipcc(["-shared"] + objects + ["-o", tmp], verbose)
+        os.replace(tmp, out)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
 
 
 def build(verbose=False):
@@ -125,6 +146,9 @@ def lib():
         L.ssm_ssd_bidir_workspace_bytes.restype = sz
         L.ssm_ssd_bidir_fwd.argtypes = [vp] * 12 + [i64] * 6 + [ci, vp, sz, vp]
         L.ssm_ssd_bidir_fwd.restype = ci
+        for name, (restype, argtypes) in _HYBRID_PROTOTYPES.items():
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = restype, argtypes
         L.ssm_status_str.argtypes = [ci]
         L.ssm_status_str.restype = ctypes.c_char_p
         _lib = L

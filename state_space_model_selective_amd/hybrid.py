@@ -1,0 +1,225 @@
+"""Binding of the hybrid block's operators (``include/ssm_hybrid.h``): the
+gated linear recurrence (``ssm_glr_*``), the norm and rotation of queries and
+keys (``ssm_qk_rope_*``) and attention with a sliding window and sinks
+(``ssm_swa_*``).
+
+As for the scan, only argument marshalling happens here: every tensor is
+checked (type, shape, layout, device) before a pointer is taken, outputs and
+workspaces that are not given are allocated, and the kernels do the rest. The
+GPU check comes last, so that each rejection also shows on CPU tensors. With
+``stream`` given, what a call allocates is allocated on that stream, so that
+its memory is not reused before the stream is done with it.
+"""
+import contextlib
+import ctypes
+
+_vp, _i64, _sz, _ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+
+GLR_CKPT_STEPS = 16
+
+# name: (restype, argtypes), as declared in ssm_hybrid.h
+PROTOTYPES = {
+    "ssm_glr_ckpt_bytes": (_sz, [_i64] * 3),
+    "ssm_glr_workspace_bytes": (_sz, [_i64] * 3 + [_ci]),
+    "ssm_glr_fwd": (_ci, [_vp] * 8 + [_i64] * 3 + [_ci, _vp, _sz, _vp]),
+    "ssm_glr_bwd_workspace_bytes": (_sz, [_i64] * 3 + [_ci]),
+    "ssm_glr_bwd": (_ci, [_vp] * 12 + [_i64] * 3 + [_ci, _vp, _sz, _vp]),
+    "ssm_glr_step": (_ci, [_vp] * 7 + [_i64] * 2 + [_ci, _vp]),
+}
+
+
+def _pkg():
+    import state_space_model_selective_amd as ssm
+    return ssm
+
+
+def _lead(where, name, t, ndim):
+    """Checks the argument that the others are checked against; its dtype code."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a torch.Tensor, got %s" % (where, name, type(t).__name__))
+    if t.dim() != ndim:
+        raise ValueError("%s: %s must have %d dimensions, got shape %s" % (where, name, ndim, tuple(t.shape)))
+    if t.dtype is torch.float32:
+        return 0
+    if t.dtype is torch.bfloat16:
+        return 1
+    raise TypeError("%s: %s must be float32 or bfloat16, got %s" % (where, name, t.dtype))
+
+
+def _refuse(where, name, t, dtype, shape, device):
+    """Says what is wrong with an argument that is not a dense tensor of this kind."""
+    import torch
+    if t is None:
+        raise ValueError("%s: %s is required" % (where, name))
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a torch.Tensor, got %s" % (where, name, type(t).__name__))
+    if t.dtype != dtype:
+        raise TypeError("%s: %s must be %s, got %s" % (where, name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s: %s is on %s, the first argument on %s" % (where, name, t.device, device))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: %s must have shape %s, got %s" % (where, name, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s: %s must be contiguous (dense row-major)" % (where, name))
+
+
+def _dense(where, name, t, dtype, shape, device):
+    """The address of a dense tensor of this dtype, shape and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(where, name, t, dtype, shape, device)
+
+
+def _maybe(where, name, t, dtype, shape, device):
+    return None if t is None else _dense(where, name, t, dtype, shape, device)
+
+
+def _gpu(where, t):
+    if not t.is_cuda:
+        raise RuntimeError("%s runs on the GPU only; its arguments are on %s" % (where, t.device))
+
+
+def _raw_stream(device, stream):
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating(device, stream):
+    """The context in which a call's outputs and workspace are allocated."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(device, stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(where, workspace, need, device):
+    """(tensor or None, address, bytes)"""
+    import torch
+    if workspace is None:
+        if not need:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("%s: workspace must be a torch.Tensor" % where)
+    if workspace.device != device:
+        raise ValueError("%s: workspace is on %s, the first argument on %s" % (where, workspace.device, device))
+    if not workspace.is_contiguous():
+        raise ValueError("%s: workspace must be contiguous" % where)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _done(rc, where):
+    if rc != 0:
+        raise _pkg().SSMError(rc, where)
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+# ---------------------------------------------------------------------------
+def ssm_glr_ckpt_shape(Bs, L, ED):
+    """Shape of the state checkpoints (float32) that ssm_glr_fwd writes for ssm_glr_bwd."""
+    return (Bs, (L + GLR_CKPT_STEPS - 1) // GLR_CKPT_STEPS, ED)
+
+
+def ssm_glr_workspace_bytes(Bs, L, ED, dtype=0):
+    return int(_pkg().lib().ssm_glr_workspace_bytes(Bs, L, ED, int(dtype)))
+
+
+def ssm_glr_bwd_workspace_bytes(Bs, L, ED, dtype=0):
+    return int(_pkg().lib().ssm_glr_bwd_workspace_bytes(Bs, L, ED, int(dtype)))
+
+
+def ssm_glr_fwd(x, gr, gi, A, y=None, h_last=None, ckpt=None, h0=None, workspace=None, stream=None):
+    """Gated linear recurrence: with r = sigmoid(gr), i = sigmoid(gi) and
+    a = exp(A r), h_t = a h_{t-1} + sqrt(max(0, 1 - a^2)) i x, y_t = h_t, from
+    h0 (zero if None). x, gr, gi and y are (Bs, L, ED); A (ED,) float32 is
+    negative. The final state goes to h_last ((Bs, ED) float32) and the states
+    that ssm_glr_bwd needs to ckpt (float32, ssm_glr_ckpt_shape(Bs, L, ED)) if
+    given. Returns y."""
+    import torch
+    where, f32 = "ssm_glr_fwd", torch.float32
+    code = _lead(where, "x", x, 3)
+    shape, dt, dev = x.shape, x.dtype, x.device
+    Bs, L, ED = shape
+    px = _dense(where, "x", x, dt, shape, dev)
+    pr, pi = _dense(where, "gr", gr, dt, shape, dev), _dense(where, "gi", gi, dt, shape, dev)
+    pA, ph0 = _dense(where, "A", A, f32, (ED,), dev), _maybe(where, "h0", h0, f32, (Bs, ED), dev)
+    py, phl = _maybe(where, "y", y, dt, shape, dev), _maybe(where, "h_last", h_last, f32, (Bs, ED), dev)
+    pck = _maybe(where, "ckpt", ckpt, f32, ssm_glr_ckpt_shape(Bs, L, ED), dev)
+    _gpu(where, x)
+    L_ = _pkg().lib()
+    with _allocating(dev, stream):
+        if y is None:
+            y = torch.empty_like(x)
+            py = y.data_ptr()
+        ws, pw, nw = _workspace(where, workspace, L_.ssm_glr_workspace_bytes(Bs, L, ED, code), dev)
+    _done(L_.ssm_glr_fwd(px, pr, pi, pA, ph0, py, phl, pck, Bs, L, ED, code, pw, nw, _raw_stream(dev, stream)), where)
+    return y
+
+
+def ssm_glr_bwd(x, gr, gi, A, ckpt, dy, dh_last=None, want_dh0=False, out=None, workspace=None, stream=None):
+    """Gradients of sum(dy * y) (+ sum(dh_last * h_last)) for y =
+    ssm_glr_fwd(x, gr, gi, A, h0=h0, ckpt=ckpt): a dict with dx, dgr, dgi
+    (like x), dA (ED,) float32 and, if want_dh0, dh0 (Bs, ED) float32. ckpt as
+    written by that call (it holds h0). Tensors given in ``out`` (same keys)
+    are written instead of new ones."""
+    import torch
+    where, f32 = "ssm_glr_bwd", torch.float32
+    code = _lead(where, "x", x, 3)
+    shape, dt, dev = x.shape, x.dtype, x.device
+    Bs, L, ED = shape
+    kinds = {"dx": (dt, shape), "dgr": (dt, shape), "dgi": (dt, shape), "dA": (f32, (ED,)), "dh0": (f32, (Bs, ED))}
+    o = dict(out or {})
+    for k, v in o.items():
+        if k not in kinds:
+            raise ValueError("%s: unknown output %r" % (where, k))
+        _dense(where, k, v, *kinds[k], dev)
+    px = _dense(where, "x", x, dt, shape, dev)
+    pr, pi = _dense(where, "gr", gr, dt, shape, dev), _dense(where, "gi", gi, dt, shape, dev)
+    pA, pdy = _dense(where, "A", A, f32, (ED,), dev), _dense(where, "dy", dy, dt, shape, dev)
+    pck = _dense(where, "ckpt", ckpt, f32, ssm_glr_ckpt_shape(Bs, L, ED), dev)
+    pdh = _maybe(where, "dh_last", dh_last, f32, (Bs, ED), dev)
+    _gpu(where, x)
+    L_ = _pkg().lib()
+    with _allocating(dev, stream):
+        for k in ("dx", "dgr", "dgi", "dA") + (("dh0",) if want_dh0 else ()):
+            if k not in o:
+                o[k] = torch.empty(kinds[k][1], dtype=kinds[k][0], device=dev)
+        ws, pw, nw = _workspace(where, workspace, L_.ssm_glr_bwd_workspace_bytes(Bs, L, ED, code), dev)
+    dh0 = o.get("dh0")
+    _done(L_.ssm_glr_bwd(px, pr, pi, pA, pck, pdy, pdh, o["dx"].data_ptr(), o["dgr"].data_ptr(), o["dgi"].data_ptr(),
+                         o["dA"].data_ptr(), None if dh0 is None else dh0.data_ptr(), Bs, L, ED, code, pw, nw,
+                         _raw_stream(dev, stream)), where)
+    return o
+
+
+def ssm_glr_step(x, gr, gi, A, h, y=None, h_out=None, stream=None):
+    """One token of ssm_glr_fwd: x, gr, gi (Bs, ED), the state h (Bs, ED)
+    float32. Returns (y, h_out); h_out=h updates the state in place."""
+    import torch
+    where, f32 = "ssm_glr_step", torch.float32
+    code = _lead(where, "x", x, 2)
+    shape, dt, dev = x.shape, x.dtype, x.device
+    Bs, ED = shape
+    px = _dense(where, "x", x, dt, shape, dev)
+    pr, pi = _dense(where, "gr", gr, dt, shape, dev), _dense(where, "gi", gi, dt, shape, dev)
+    pA, ph = _dense(where, "A", A, f32, (ED,), dev), _dense(where, "h", h, f32, shape, dev)
+    py, pho = _maybe(where, "y", y, dt, shape, dev), _maybe(where, "h_out", h_out, f32, shape, dev)
+    _gpu(where, x)
+    with _allocating(dev, stream):
+        if y is None:
+            y = torch.empty_like(x)
+            py = y.data_ptr()
+        if h_out is None:
+            h_out = torch.empty_like(h)
+            pho = h_out.data_ptr()
+    _done(_pkg().lib().ssm_glr_step(px, pr, pi, pA, ph, py, pho, Bs, ED, code, _raw_stream(dev, stream)), where)
+    return y, h_out

@@ -1,0 +1,111 @@
+"""64-bit definitions of the hybrid block's operators, on the CPU, with the
+error that the kernels' roundings can add to each value (test infrastructure).
+
+A rounding to float32 is off by at most EPS = 2^-24 relative to the value; the
+constants count how many of them reach a value (each hardware exponential,
+reciprocal and square root counts as two, being within one step).
+"""
+import math
+
+import torch
+
+EPS = torch.finfo(torch.float32).eps / 2
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def within(name, got, ref, bound):
+    """|got - ref| <= bound everywhere (ref finite); says where it is worst."""
+    got, ref = got.detach().double().cpu(), ref.double()
+    assert got.shape == ref.shape, (name, got.shape, ref.shape)
+    if not got.numel():
+        return
+    assert bool(torch.isfinite(got).all()), "%s: not finite at %s" % (name, (~torch.isfinite(got)).nonzero()[0].tolist())
+    over = ((got - ref).abs() - bound).flatten()
+    i = int(over.argmax())
+    assert float(over[i]) <= 0, "%s: %.9g for %.9g, off by %.3g, allowed %.3g (flat index %d)" % (
+        name, got.flatten()[i], ref.flatten()[i], abs(float(got.flatten()[i] - ref.flatten()[i])),
+        float(bound.flatten()[i]), i)
+
+
+def rounded(ref, err, dtype):
+    """The error bound of a value stored in dtype: err before the store, then half a step (and the denormal range)."""
+    if dtype == torch.float32:
+        return err + EPS * ref.abs() + 1e-37
+    return err + half_step(dtype) * (ref.abs() + err) + 1e-37
+
+
+# ---------------------------------------------------------------------------
+# gated linear recurrence
+# ---------------------------------------------------------------------------
+def glr_inputs(Bs, L, ED, dtype, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)
+    return dict(x=r(Bs, L, ED).to(dtype), gr=(spread * r(Bs, L, ED)).to(dtype), gi=(spread * r(Bs, L, ED)).to(dtype),
+                A=-torch.exp(torch.empty(ED).uniform_(math.log(0.004), math.log(2.0), generator=g)),
+                h0=r(Bs, ED), dy=r(Bs, L, ED).to(dtype), dh_last=r(Bs, ED))
+
+
+def glr_reference(x, gr, gi, A, h0=None, dy=None, dh_last=None, **_):
+    """{name: (value, error before the store)} of y, h_last and, with dy, the gradients.
+
+    A value of a: the argument A2 r has r's error (2 + 2 + |gr| + 2 roundings,
+    times |la|) and its own rounding, the exponential two: 8 + |la| (7 + |gr|).
+    A value of s: sqrt halves the relative error of 1 - a^2, which is that of
+    la (series, at most 8 roundings) or 2 a^2 / (1 - a^2) < 7 times that of a;
+    i has 6 + |gi|, the products two more."""
+    x, gr, gi, A = x.double(), gr.double(), gi.double(), A.double()
+    Bs, L, ED = x.shape
+    h = torch.zeros(Bs, ED, dtype=torch.float64) if h0 is None else h0.double()
+    r, i = torch.sigmoid(gr), torch.sigmoid(gi)
+    la = A * r
+    a, s = la.exp(), (-torch.expm1(2 * la)).clamp(min=0).sqrt()
+    ea = EPS * (8 + la.abs() * (7 + gr.abs()))              # relative, of a
+    es = EPS * (10 + (7 + gr.abs())) + 4 * ea               # relative, of s
+    u = s * i * x
+    eu = u.abs() * (es + EPS * (8 + gi.abs()))
+    hs, es_h = torch.empty_like(x), torch.empty_like(x)
+    h_init, err = h, torch.zeros_like(h)
+    for t in range(L):
+        new = a[:, t] * h + u[:, t]
+        # (the last term: the products of a over a chunk and the joins round a few times more)
+        err = a[:, t] * err + (a[:, t] * h.abs()) * (ea[:, t] + 3 * EPS) + eu[:, t] + EPS * new.abs()
+        h = new
+        hs[:, t], es_h[:, t] = h, err
+    out = {"y": (hs, es_h), "h_last": (h, err)}
+    if dy is None:
+        return out
+    dy = dy.double()
+    g_all, eg_all = torch.empty_like(x), torch.empty_like(x)
+    G = torch.zeros(Bs, ED, dtype=torch.float64) if dh_last is None else dh_last.double()
+    eG = torch.zeros_like(G)
+    for t in range(L - 1, -1, -1):
+        g = dy[:, t] + G
+        eg = eG + EPS * g.abs()
+        g_all[:, t], eg_all[:, t] = g, eg
+        G = a[:, t] * g
+        eG = a[:, t] * eg + G.abs() * (ea[:, t] + 3 * EPS)
+    hp = torch.cat([h_init.unsqueeze(1), hs[:, :-1]], 1)
+    ehp = torch.cat([torch.zeros_like(h_init).unsqueeze(1), es_h[:, :-1]], 1)
+    ix, g = i * x, g_all
+    root = torch.where(s > 0, a * a / torch.where(s > 0, s, torch.ones_like(s)), torch.zeros_like(s)) * ix
+    e_root = root.abs() * (2 * ea + es + EPS * (12 + gi.abs()))
+    er = EPS * (6 + gr.abs())
+    inner = a * hp - root
+    e_inner = a * ehp + (a * hp).abs() * (ea + EPS) + e_root + EPS * inner.abs()
+    dlr = g * inner * r
+    e_dlr = (eg_all * inner.abs() + g.abs() * e_inner) * r + dlr.abs() * (er + 3 * EPS)
+    dx = g * s * i
+    dgi = dx * x * (1 - i)
+    dgr = dlr * A * (1 - r)
+    e_dx = eg_all * s * i + dx.abs() * (es + EPS * (8 + gi.abs()))
+    # (1 - i and 1 - r are off by an absolute rounding)
+    e_dgi = e_dx * x.abs() * (1 - i) + dgi.abs() * 3 * EPS + (dx * x).abs() * EPS * (7 + gi.abs())
+    e_dgr = e_dlr * A.abs() * (1 - r) + dgr.abs() * 3 * EPS + (dlr * A).abs() * EPS * (7 + gr.abs())
+    terms = Bs * L
+    dA = dlr.sum((0, 1))
+    e_dA = e_dlr.sum((0, 1)) + EPS * min(terms, 600) * dlr.abs().sum((0, 1))
+    out.update(dx=(dx, e_dx), dgr=(dgr, e_dgr), dgi=(dgi, e_dgi), dA=(dA, e_dA), dh0=(G, eG))
+    return out

@@ -1,0 +1,222 @@
+"""The gated linear recurrence on the GPU against its 64-bit definition."""
+import pytest
+import torch
+
+import state_space_model_selective_amd as ssm
+from hybrid_util import glr_inputs, glr_reference, rounded, within
+from parity_util import log
+from test_graph_gpu import replay_check
+
+pytestmark = pytest.mark.gpu
+
+f32, bf16 = torch.float32, torch.bfloat16
+# one step, lengths around the checkpoint spacing and the chunks, prime and long ones; odd and tiny channel counts
+SIZES = [(1, 1, 1), (2, 1, 8), (3, 2, 3), (1, 15, 4), (2, 16, 7), (2, 17, 12), (1, 33, 130), (2, 128, 64),
+         (2, 129, 20), (1, 1009, 33), (3, 700, 128), (1, 3001, 8), (150, 3, 4), (1, 260, 1028)]
+
+
+def cuda(t):
+    return {k: v.cuda() for k, v in t.items()}
+
+
+def check(t, out, dtype, **kw):
+    ref = glr_reference(**{**t, **kw})
+    for name, got in out.items():
+        value, err = ref[name]
+        assert got.dtype == (dtype if name in ("y", "dx", "dgr", "dgi") else f32)
+        within(name, got, value, rounded(value, err, got.dtype))
+
+
+def train(g, h0=True, dh_last=True):
+    Bs, L, ED = g["x"].shape
+    h_last = torch.full((Bs, ED), float("nan"), device="cuda")
+    ckpt = torch.full(ssm.ssm_glr_ckpt_shape(Bs, L, ED), float("nan"), device="cuda")
+    y = ssm.ssm_glr_fwd(g["x"], g["gr"], g["gi"], g["A"], h0=g["h0"] if h0 else None, h_last=h_last, ckpt=ckpt)
+    grads = ssm.ssm_glr_bwd(g["x"], g["gr"], g["gi"], g["A"], ckpt, g["dy"], dh_last=g["dh_last"] if dh_last else None,
+                            want_dh0=True)
+    return {"y": y, "h_last": h_last, **grads}
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("Bs,L,ED", SIZES)
+def test_forward_and_gradients(Bs, L, ED, dtype):
+    log("glr %d x %d x %d %s" % (Bs, L, ED, dtype))
+    t = glr_inputs(Bs, L, ED, dtype, seed=L + ED)
+    check(t, train(cuda(t)), dtype)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_without_states(dtype):
+    t = glr_inputs(2, 200, 24, dtype, seed=5)
+    check(t, train(cuda(t), h0=False, dh_last=False), dtype, h0=None, dh_last=None)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_forward_alone_gives_the_same(dtype):
+    g = cuda(glr_inputs(2, 300, 40, dtype, seed=6))
+    y = ssm.ssm_glr_fwd(g["x"], g["gr"], g["gi"], g["A"], h0=g["h0"])
+    assert torch.equal(y, train(g)["y"])
+
+
+def test_wide_logits():
+    """Gates from shut to open: logits of some tens, where the decay is 1 or the input is cut off."""
+    t = glr_inputs(2, 90, 32, f32, seed=7, spread=15.0)
+    check(t, train(cuda(t)), f32)
+
+
+def test_shut_and_open_gates():
+    """Infinite logits and a zero rate: decay exactly 1 without input, zero gradients instead of NaN."""
+    t = glr_inputs(1, 70, 8, f32, seed=8)
+    t["gr"][:, 10] = float("-inf")
+    t["gr"][:, 11] = float("inf")
+    t["gi"][:, 12] = float("-inf")
+    t["gr"][:, 13] = -200.0
+    t["A"][3] = 0.0
+    out = train(cuda(t))
+    assert torch.equal(out["y"][:, 10], out["y"][:, 9])
+    assert torch.equal(out["y"][0, :, 3].cpu(), t["h0"][0, 3].expand(70))
+    for k, v in out.items():
+        assert bool(torch.isfinite(v).all()), k
+    assert float(out["dgr"][:, 10].abs().max()) == 0 and float(out["dx"][:, 10].abs().max()) == 0
+    keep = [c for c in range(8) if c != 3]
+    finite = dict(t, gr=t["gr"].clone().clamp(-200, 200), gi=t["gi"].clone().clamp(-200, 200))
+    ref = glr_reference(**finite)
+    within("y", out["y"][..., keep], ref["y"][0][..., keep], rounded(*ref["y"], f32)[..., keep])
+    within("dA", out["dA"][keep], ref["dA"][0][keep], rounded(*ref["dA"], f32)[keep])
+
+
+def test_growing_channel_takes_no_input():
+    t = glr_inputs(1, 40, 4, f32, seed=9)
+    t["A"] = t["A"].abs()
+    check(t, train(cuda(t)), f32)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_input_stays_in_its_channel(bad):
+    t = glr_inputs(1, 300, 8, f32, seed=10)
+    clean = train(cuda(t))
+    t["x"][0, 100, 5] = bad
+    out = train(cuda(t))
+    keep = [c for c in range(8) if c != 5]
+    for k, v in out.items():
+        assert torch.equal(v[..., keep], clean[k][..., keep]), k
+    assert torch.equal(out["y"][:, :100], clean["y"][:, :100])
+    assert not bool(torch.isfinite(out["y"][0, 100:, 5]).any())
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_resumed_in_pieces(dtype):
+    t = glr_inputs(2, 150, 20, dtype, seed=11)
+    g, ref = cuda(t), glr_reference(**t)
+    h, ys = g["h0"], []
+    for lo, hi in ((0, 1), (1, 40), (40, 150)):
+        last = torch.empty_like(h)
+        ys.append(ssm.ssm_glr_fwd(*(g[n][:, lo:hi].contiguous() for n in ("x", "gr", "gi")), g["A"], h0=h, h_last=last))
+        h = last
+    within("y", torch.cat(ys, 1), ref["y"][0], rounded(*ref["y"], dtype))
+    within("h_last", h, ref["h_last"][0], rounded(*ref["h_last"], f32))
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("Bs,ED", [(1, 1), (3, 7), (5, 260), (256, 64)])
+def test_step(Bs, ED, dtype):
+    t = glr_inputs(Bs, 1, ED, dtype, seed=Bs + ED)
+    g, ref = cuda(t), glr_reference(**t)
+    one = [g[n][:, 0].contiguous() for n in ("x", "gr", "gi")]
+    y, h = ssm.ssm_glr_step(*one, g["A"], g["h0"])
+    within("y", y, ref["y"][0][:, 0], rounded(*ref["y"], dtype)[:, 0])
+    within("h", h, ref["h_last"][0], rounded(*ref["h_last"], f32))
+    state = g["h0"].clone()
+    y2, same = ssm.ssm_glr_step(*one, g["A"], state, h_out=state)
+    assert same is state and torch.equal(state, h) and torch.equal(y2, y)
+
+
+def test_empty():
+    dev = torch.device("cuda:0")
+    z = lambda *s: torch.zeros(*s, device=dev)
+    h0, last = torch.randn(2, 5, device=dev), torch.full((2, 5), float("nan"), device=dev)
+    A = -torch.ones(5, device=dev)
+    assert ssm.ssm_glr_fwd(z(2, 0, 5), z(2, 0, 5), z(2, 0, 5), A, h0=h0, h_last=last).shape == (2, 0, 5)
+    assert torch.equal(last, h0)
+    ssm.ssm_glr_fwd(z(2, 0, 5), z(2, 0, 5), z(2, 0, 5), A, h_last=last)
+    assert float(last.abs().max()) == 0
+    g = ssm.ssm_glr_bwd(z(2, 0, 5), z(2, 0, 5), z(2, 0, 5), A, z(2, 0, 5), z(2, 0, 5), dh_last=h0, want_dh0=True)
+    assert torch.equal(g["dh0"], h0) and float(g["dA"].abs().max()) == 0
+    assert ssm.ssm_glr_fwd(z(0, 4, 5), z(0, 4, 5), z(0, 4, 5), A).shape == (0, 4, 5)
+    assert ssm.ssm_glr_fwd(z(2, 4, 0), z(2, 4, 0), z(2, 4, 0), A[:0]).shape == (2, 4, 0)
+    y, h = ssm.ssm_glr_step(z(0, 5), z(0, 5), z(0, 5), A, z(0, 5))
+    assert y.shape == h.shape == (0, 5)
+
+
+def test_gradient_against_differences():
+    """<gradient, v> against the central difference of the loss along v: the loss's own rounding (relative 1e-5 of its
+    terms' sum here) over the step, plus the third-order term."""
+    t = cuda(glr_inputs(2, 64, 16, f32, seed=12))
+    names = ("x", "gr", "gi", "A", "h0")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = {n: torch.randn(t[n].shape, generator=gen, device="cuda") * (0.05 if n == "A" else 1.0) for n in names}
+
+    def loss(step):
+        s = {n: t[n] + step * v[n] for n in names}
+        last = torch.empty_like(s["h0"])
+        y = ssm.ssm_glr_fwd(s["x"], s["gr"], s["gi"], s["A"], h0=s["h0"], h_last=last)
+        return float((y.double() * t["dy"].double()).sum() + (last.double() * t["dh_last"].double()).sum())
+
+    out = train(t)
+    want = sum(float((out["d" + n].double() * v[n].double()).sum()) for n in names)
+    eps = 1e-2
+    got = (8 * (loss(eps) - loss(-eps)) - (loss(2 * eps) - loss(-2 * eps))) / (12 * eps)  # fourth order
+    assert abs(got - want) <= 2e-3 * max(1.0, sum(float((out["d" + n] * v[n]).abs().sum()) for n in names) ** 0.5), (got, want)
+
+
+def test_repeated_calls_are_identical():
+    g = cuda(glr_inputs(2, 2000, 64, bf16, seed=13))
+    first = train(g)
+    for _ in range(5):
+        for k, v in train(g).items():
+            assert torch.equal(v, first[k]), k
+
+
+def test_on_another_stream():
+    t = glr_inputs(1, 1500, 64, f32, seed=14)
+    g = cuda(t)
+    want = train(g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ckpt = torch.empty(ssm.ssm_glr_ckpt_shape(1, 1500, 64), device="cuda")
+    y = ssm.ssm_glr_fwd(g["x"], g["gr"], g["gi"], g["A"], h0=g["h0"], ckpt=ckpt, stream=side)
+    grads = ssm.ssm_glr_bwd(g["x"], g["gr"], g["gi"], g["A"], ckpt, g["dy"], dh_last=g["dh_last"], stream=side)
+    side.synchronize()
+    assert torch.equal(y, want["y"])
+    for k, v in grads.items():
+        assert torch.equal(v, want[k]), k
+
+
+@pytest.mark.parametrize("Bs,L,ED", [(1, 2500, 64), (2, 40, 7)])
+def test_graph(Bs, L, ED):
+    g = cuda(glr_inputs(Bs, L, ED, bf16, seed=15))
+    out = train(g)
+    ckpt = torch.empty(ssm.ssm_glr_ckpt_shape(Bs, L, ED), device="cuda")
+    y, last = torch.empty_like(out["y"]), torch.empty_like(out["h_last"])
+    grads = {k: torch.empty_like(out[k]) for k in ("dx", "dgr", "dgi", "dA", "dh0")}
+
+    def both():
+        ssm.ssm_glr_fwd(g["x"], g["gr"], g["gi"], g["A"], y=y, h0=g["h0"], h_last=last, ckpt=ckpt)
+        ssm.ssm_glr_bwd(g["x"], g["gr"], g["gi"], g["A"], ckpt, g["dy"], dh_last=g["dh_last"], out=grads)
+
+    replay_check("gated recurrence", both, [y, last] + list(grads.values()))
+
+
+def test_long_offsets():
+    """Elements past 2^31: the last channels of a tensor that large are those of a short copy of them."""
+    Bs, L, ED = 1, 1 << 19, 4104  # 2.15e9 elements of bf16
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(Bs, L, ED, dtype=bf16, device="cuda")
+    tail = torch.randn(L, 8, generator=gen, device="cuda").to(bf16)
+    x.zero_()
+    x[0, :, -8:] = tail
+    A = torch.full((ED,), -0.3, device="cuda")
+    y = ssm.ssm_glr_fwd(x, x, x, A)
+    few = tail[-4096:].unsqueeze(0).contiguous()  # (the decay over 4096 steps leaves nothing of what came before)
+    ref = ssm.ssm_glr_fwd(few, few, few, A[:8].contiguous())
+    assert torch.allclose(y[0, -512:, -8:].float(), ref[0, -512:].float(), rtol=2 ** -7, atol=1e-6)
