@@ -93,6 +93,60 @@ int ssm_glr_bwd(const void* x, const void* gr, const void* gi, const float* A, c
 int ssm_glr_step(const void* x, const void* gr, const void* gi, const float* A, const float* h, void* y,
                  float* h_out, int64_t Bs, int64_t ED, int dtype, void* stream);
 
+/*
+ * Norm and rotation of queries and keys, for each head, in one pass. For a
+ * head's D entries x, weight w and position p:
+ *
+ *   n_j = x_j w_j / sqrt(mean(x^2) + eps)
+ *   (o_j, o_{j+R/2}) = (n_j cos - n_{j+R/2} sin, n_{j+R/2} cos + n_j sin),  j < R/2,
+ *   at the angle p freq[j];   o_j = n_j for j >= R
+ *
+ * Angles are reduced in 64 bits, so positions of any int32 value keep their
+ * phase to the last bits of freq.
+ *   q, k   : (Bs, L, Hq, D), (Bs, L, Hk, D) of dtype, strided by qs, ks
+ *   wq, wk : (D) float32, or NULL (ones)
+ *   freq   : (R / 2) float64, radians per position; NULL when R is 0
+ *   pos    : (Bs, L) int32, or NULL: token t is at position t
+ *   q_out, k_out : (Bs, L, Hq, D), (Bs, L, Hk, D) of dtype, dense
+ * Supported: D 64 or 128, R a multiple of 16 in [0, D], eps >= 0 (else
+ * SSM_ERR_ARG), Hq and Hk >= 0.
+ */
+int ssm_qk_rope_fwd(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks, const float* wq,
+                    const float* wk, const double* freq, const int32_t* pos, double eps, void* q_out, void* k_out,
+                    int64_t Bs, int64_t L, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int dtype, void* stream);
+
+/*
+ * Backward pass: from dq_out, dk_out (dense, like the outputs) and the
+ * forward's inputs the gradients dq, dk (dense, of dtype) and dwq, dwk ((D)
+ * float32, or NULL: not computed), the latter summed over rows, tokens and
+ * heads in a fixed order. workspace: ssm_qk_rope_bwd_workspace_bytes().
+ */
+size_t ssm_qk_rope_bwd_workspace_bytes(int64_t Bs, int64_t L, int64_t Hq, int64_t Hk, int64_t D, int dtype);
+int ssm_qk_rope_bwd(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks, const float* wq,
+                    const float* wk, const double* freq, const int32_t* pos, double eps, const void* dq_out,
+                    const void* dk_out, void* dq, void* dk, float* dwq, float* dwk, int64_t Bs, int64_t L, int64_t Hq,
+                    int64_t Hk, int64_t D, int64_t R, int dtype, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/*
+ * Appends L new tokens of every row to a window cache, queries and keys
+ * normed and turned on the way. Row b's tokens stand at positions pos[b],
+ * pos[b] + 1, ... (pos: (Bs) int32; a row with pos[b] < 0 is inactive: its
+ * q_out is zero and its cache stays). The cache keeps the first `sinks`
+ * tokens and the last `window` others: position p lives in slot p when p <
+ * sinks, else in slot sinks + (p - sinks) mod window. Of several new tokens
+ * for one slot the last stays.
+ *   v : (Bs, L, Hk, D) of dtype, strided by vs: copied to the cache
+ *   k_cache, v_cache : (Bs, Hk, sinks + window, D) of dtype, dense
+ *   q_out : (Bs, L, Hq, D) of dtype, dense
+ * window >= 1 and sinks >= 0, sinks + window < 2^31 (else SSM_ERR_DIM).
+ */
+int ssm_qk_rope_append(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks, const void* v,
+                       const ssm_strides* vs, const float* wq, const float* wk, const double* freq,
+                       const int32_t* pos, double eps, void* q_out, void* k_cache, void* v_cache, int64_t Bs,
+                       int64_t L, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t window, int64_t sinks,
+                       int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

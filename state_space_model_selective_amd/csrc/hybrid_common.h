@@ -1,0 +1,119 @@
+// Internal helpers of the hybrid block's operators (not part of the public
+// C ABI): vector access and the host's checks of buffers.
+#ifndef SSM_HYBRID_COMMON_H
+#define SSM_HYBRID_COMMON_H
+
+#include "ssm_hybrid.h"
+
+#include "scan_common.h"
+
+namespace {
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+// ---------------------------------------------------------------------------
+// 16-byte element access: 4 float32 or 8 bfloat16
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void widen(uint4 u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x), v[1] = __uint_as_float(u.y), v[2] = __uint_as_float(u.z), v[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+
+// two floats rounded to nearest even as a bfloat16 pair (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  bf2 p;
+  p[0] = static_cast<__bf16>(lo);
+  p[1] = static_cast<__bf16>(hi);
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+template <>
+struct Vec16<uint16_t> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void widen(uint4 u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+
+// dst[c] = sum over rows of part (rows, cols), in a fixed order: 16 threads of
+// a column each sum every 16th row, their sums are added in thread order.
+__global__ __launch_bounds__(256) void sum_rows_kernel(const float* part, float* dst, int64_t rows, int64_t cols) {
+  __shared__ float sum[16][17];
+  const int ce = threadIdx.x & 15, cr = threadIdx.x >> 4;
+  const int64_t e = blockIdx.x * 16ll + ce;
+  float v = 0.f;
+  if (e < cols)
+    for (int64_t r = cr; r < rows; r += 16) v += part[r * cols + e];
+  sum[cr][ce] = v;
+  __syncthreads();
+  if (cr == 0 && e < cols) {
+    for (int j = 1; j < 16; ++j) v += sum[j][ce];
+    dst[e] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host: buffers of one call
+// ---------------------------------------------------------------------------
+struct Buf {
+  const void* p;
+  int64_t bytes;
+  bool required, out;
+};
+
+// Null, alignment and overlap of the buffers of one call (an output overlaps
+// nothing; inputs may overlap each other).
+int check_bufs(const Buf* v, int n) {
+  for (int i = 0; i < n; ++i)
+    if (v[i].required && v[i].bytes > 0 && !v[i].p) return SSM_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (v[i].p && !aligned16(v[i].p)) return SSM_ERR_UNSUPPORTED;
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j)
+      if (i != j && v[i].out && v[i].p && v[j].p && v[i].bytes > 0 && v[j].bytes > 0 &&
+          overlap(rng(v[i].p, v[i].bytes), rng(v[j].p, v[j].bytes)))
+        return SSM_ERR_ALIAS;
+  return SSM_OK;
+}
+
+// The strides of a (batch, token, head, D) argument (dense where s is null)
+// and the bytes from its first to its last element.
+int strided(const ssm_strides* s, int64_t Bs, int64_t L, int64_t H, int64_t D, int es, ssm_strides* out,
+            int64_t* bytes) {
+  int64_t tok, row, all;
+  if (!mul_nn(H, D, &tok) || !mul_nn(L, tok, &row) || !mul_nn(Bs, row, &all) || !mul_nn(all, 8, bytes))
+    return SSM_ERR_DIM;
+  *out = s ? *s : ssm_strides{row, tok, D};
+  if (out->batch < 0 || out->token < 0 || out->head < 0) return SSM_ERR_UNSUPPORTED;
+  if ((out->batch * es) % 16 || (out->token * es) % 16 || (out->head * es) % 16) return SSM_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (all == 0) return SSM_OK;
+  int64_t a, b, c;
+  if (!mul_nn(Bs - 1, out->batch, &a) || !mul_nn(L - 1, out->token, &b) || !mul_nn(H - 1, out->head, &c))
+    return SSM_ERR_DIM;
+  constexpr int64_t kMost = INT64_MAX / 64;
+  if (a > kMost || b > kMost || c > kMost || D > kMost) return SSM_ERR_DIM;
+  *bytes = (a + b + c + D) * es;
+  return SSM_OK;
+}
+
+}  // namespace
+
+#endif  // SSM_HYBRID_COMMON_H

@@ -8,9 +8,7 @@
 // (P, H) of every chunk, a second folds them along the sequence into the
 // state entering each chunk, the third runs every chunk from that state.
 // The backward does the same with the adjoint, in reverse time.
-#include "ssm_hybrid.h"
-
-#include "scan_common.h"
+#include "hybrid_common.h"
 
 namespace {
 
@@ -273,23 +271,6 @@ __global__ __launch_bounds__(256) void glr_bwd_apply_kernel(const GlrArgs<T> p) 
   for (int c = 0; c < VEC; ++c) p.dA_part[(b * p.nchunks + k) * p.ED + e + c] = dA[c];
 }
 
-// dA[e] = sum over rows of part (rows, ED), in a fixed order: 16 threads of a
-// channel each sum every 16th row, their sums are added in thread order.
-__global__ __launch_bounds__(256) void glr_dA_kernel(const float* part, float* dA, int64_t rows, int64_t ED) {
-  __shared__ float sum[16][17];
-  const int ce = threadIdx.x & 15, cr = threadIdx.x >> 4;
-  const int64_t e = blockIdx.x * 16ll + ce;
-  float v = 0.f;
-  if (e < ED)
-    for (int64_t r = cr; r < rows; r += 16) v += part[r * ED + e];
-  sum[cr][ce] = v;
-  __syncthreads();
-  if (cr == 0 && e < ED) {
-    for (int j = 1; j < 16; ++j) v += sum[j][ce];
-    dA[e] = v;
-  }
-}
-
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void glr_step_kernel(const T* x, const T* gr, const T* gi, const float* A,
                                                        const float* h, T* y, float* h_out, int64_t Bs, int64_t ED) {
@@ -335,29 +316,6 @@ int glr_sizes(int64_t Bs, int64_t L, int64_t ED, int dtype, int64_t* n, int64_t*
   return SSM_OK;
 }
 
-struct Buf {
-  const void* p;
-  int64_t bytes;
-  bool required, out;
-};
-
-// Null, alignment and overlap of the buffers of one call (an output overlaps
-// nothing; inputs may overlap each other).
-int check_bufs(const Buf* v, int n) {
-  for (int i = 0; i < n; ++i)
-    if (v[i].required && v[i].bytes > 0 && !v[i].p) return SSM_ERR_NULL;
-  for (int i = 0; i < n; ++i)
-    if (v[i].p && !aligned16(v[i].p)) return SSM_ERR_UNSUPPORTED;
-  for (int i = 0; i < n; ++i)
-    for (int j = 0; j < n; ++j)
-      if (i != j && v[i].out && v[i].p && v[j].p && v[i].bytes > 0 && v[j].bytes > 0 &&
-          overlap(rng(v[i].p, v[i].bytes), rng(v[j].p, v[j].bytes)))
-        return SSM_ERR_ALIAS;
-  return SSM_OK;
-}
-
-constexpr int64_t kMaxGrid = 0x7fffffff;
-
 size_t glr_agg_bytes(const GlrPlan& pl, int64_t c) { return static_cast<size_t>(pl.nchunks * c) * 8; }
 size_t glr_enter_bytes(const GlrPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 4 + 15) & ~size_t(15); }
 
@@ -386,7 +344,7 @@ int launch_bwd(GlrArgs<T> a, float* dA, hipStream_t st) {
   hipLaunchKernelGGL(glr_join_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64), 0, st, a.agg, a.dh_last,
                      a.enter, n, a.nchunks, a.ED, 1);
   hipLaunchKernelGGL((glr_bwd_apply_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(glr_dA_kernel, dim3(static_cast<unsigned>((a.ED + 15) / 16)), dim3(256), 0, st, a.dA_part, dA,
+  hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>((a.ED + 15) / 16)), dim3(256), 0, st, a.dA_part, dA,
                      a.Bs * a.nchunks, a.ED);
   return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }

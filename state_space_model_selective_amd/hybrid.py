@@ -13,7 +13,7 @@ its memory is not reused before the stream is done with it.
 import contextlib
 import ctypes
 
-_vp, _i64, _sz, _ci = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+_vp, _i64, _sz, _ci, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_double
 
 GLR_CKPT_STEPS = 16
 
@@ -25,7 +25,16 @@ PROTOTYPES = {
     "ssm_glr_bwd_workspace_bytes": (_sz, [_i64] * 3 + [_ci]),
     "ssm_glr_bwd": (_ci, [_vp] * 12 + [_i64] * 3 + [_ci, _vp, _sz, _vp]),
     "ssm_glr_step": (_ci, [_vp] * 7 + [_i64] * 2 + [_ci, _vp]),
+    "ssm_qk_rope_fwd": (_ci, [_vp] * 8 + [_f64] + [_vp] * 2 + [_i64] * 6 + [_ci, _vp]),
+    "ssm_qk_rope_bwd_workspace_bytes": (_sz, [_i64] * 5 + [_ci]),
+    "ssm_qk_rope_bwd": (_ci, [_vp] * 8 + [_f64] + [_vp] * 6 + [_i64] * 6 + [_ci, _vp, _sz, _vp]),
+    "ssm_qk_rope_append": (_ci, [_vp] * 10 + [_f64] + [_vp] * 3 + [_i64] * 8 + [_ci, _vp]),
 }
+
+
+class SSMStrides(ctypes.Structure):
+    """ssm_strides: elements from one batch row, token and head to the next."""
+    _fields_ = [("batch", _i64), ("token", _i64), ("head", _i64)]
 
 
 def _pkg():
@@ -75,6 +84,21 @@ def _dense(where, name, t, dtype, shape, device):
 
 def _maybe(where, name, t, dtype, shape, device):
     return None if t is None else _dense(where, name, t, dtype, shape, device)
+
+
+def _strided(where, name, t, dtype, shape, device):
+    """Address and strides (None when dense) of a tensor (batch, token, head, D) whose last dimension is contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device:
+            if t.is_contiguous():
+                return t.data_ptr(), None
+            b, l, h, d = t.stride()
+            if d == 1:
+                return t.data_ptr(), ctypes.byref(SSMStrides(b, l, h))
+            raise ValueError("%s: the last dimension of %s must be contiguous" % (where, name))
+    except AttributeError:
+        pass
+    _refuse(where, name, t, dtype, shape, device)
 
 
 def _gpu(where, t):
@@ -223,3 +247,124 @@ def ssm_glr_step(x, gr, gi, A, h, y=None, h_out=None, stream=None):
             pho = h_out.data_ptr()
     _done(_pkg().lib().ssm_glr_step(px, pr, pi, pA, ph, py, pho, Bs, ED, code, _raw_stream(dev, stream)), where)
     return y, h_out
+
+
+# ---------------------------------------------------------------------------
+# norm and rotation of queries and keys
+# ---------------------------------------------------------------------------
+def _rope_args(where, q, k, wq, wk, freq, eps):
+    """The arguments that all three calls share: (dims, dtype code, addresses up to freq, eps)."""
+    import torch
+    code = _lead(where, "q", q, 4)
+    dt, dev = q.dtype, q.device
+    Bs, L, Hq, D = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("%s: k must be a 4-D tensor (Bs, L, Hk, D)" % where)
+    Hk = k.shape[2]
+    pq, sq = _strided(where, "q", q, dt, (Bs, L, Hq, D), dev)
+    pk, sk = _strided(where, "k", k, dt, (Bs, L, Hk, D), dev)
+    pwq, pwk = _maybe(where, "wq", wq, torch.float32, (D,), dev), _maybe(where, "wk", wk, torch.float32, (D,), dev)
+    R = 0
+    pf = None
+    if freq is not None:
+        if not isinstance(freq, torch.Tensor) or freq.dim() != 1:
+            raise ValueError("%s: freq must be a 1-D tensor (half the rotated entries) or None" % where)
+        R = 2 * freq.shape[0]
+        pf = _dense(where, "freq", freq, torch.float64, freq.shape, dev)
+    return (Bs, L, Hq, Hk, D, R), code, (pq, sq, pk, sk, pwq, pwk, pf), float(eps)
+
+
+def ssm_qk_rope_fwd(q, k, wq, wk, freq, pos=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norm and rotation of each head of q (Bs, L, Hq, D) and k (Bs, L, Hk, D),
+    which may be slices of a packed projection (last dimension contiguous):
+    x w / sqrt(mean(x^2) + eps), then the pairs (j, j + R/2) of the first R =
+    2 len(freq) entries turned by pos * freq[j]. wq, wk (D,) float32 or None
+    (ones); freq (R/2,) float64 radians per position, or None (no rotation);
+    pos (Bs, L) int32, or None (token t at position t). Returns (q_out,
+    k_out), dense."""
+    import torch
+    where = "ssm_qk_rope_fwd"
+    (Bs, L, Hq, Hk, D, R), code, head, eps = _rope_args(where, q, k, wq, wk, freq, eps)
+    dt, dev = q.dtype, q.device
+    pp = _maybe(where, "pos", pos, torch.int32, (Bs, L), dev)
+    pqo = _maybe(where, "q_out", q_out, dt, (Bs, L, Hq, D), dev)
+    pko = _maybe(where, "k_out", k_out, dt, (Bs, L, Hk, D), dev)
+    _gpu(where, q)
+    with _allocating(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((Bs, L, Hq, D), dtype=dt, device=dev)
+            pqo = q_out.data_ptr()
+        if k_out is None:
+            k_out = torch.empty((Bs, L, Hk, D), dtype=dt, device=dev)
+            pko = k_out.data_ptr()
+    _done(_pkg().lib().ssm_qk_rope_fwd(*head, pp, eps, pqo, pko, Bs, L, Hq, Hk, D, R, code, _raw_stream(dev, stream)),
+          where)
+    return q_out, k_out
+
+
+def ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, dtype=0):
+    return int(_pkg().lib().ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, int(dtype)))
+
+
+def ssm_qk_rope_bwd(q, k, wq, wk, freq, dq_out, dk_out, pos=None, eps=1e-6, out=None, workspace=None, stream=None):
+    """Gradients of ssm_qk_rope_fwd's inputs from those of its outputs
+    (dense): a dict with dq, dk (dense, like the outputs) and, for the weights
+    that are given, dwq and dwk (D,) float32. Tensors given in ``out`` (same
+    keys) are written instead of new ones."""
+    import torch
+    where, f32 = "ssm_qk_rope_bwd", torch.float32
+    (Bs, L, Hq, Hk, D, R), code, head, eps = _rope_args(where, q, k, wq, wk, freq, eps)
+    dt, dev = q.dtype, q.device
+    kinds = {"dq": (dt, (Bs, L, Hq, D)), "dk": (dt, (Bs, L, Hk, D)), "dwq": (f32, (D,)), "dwk": (f32, (D,))}
+    o = dict(out or {})
+    for n, t in o.items():
+        if n not in kinds:
+            raise ValueError("%s: unknown output %r" % (where, n))
+        _dense(where, n, t, *kinds[n], dev)
+    pp = _maybe(where, "pos", pos, torch.int32, (Bs, L), dev)
+    pdq, pdk = _dense(where, "dq_out", dq_out, *kinds["dq"], dev), _dense(where, "dk_out", dk_out, *kinds["dk"], dev)
+    _gpu(where, q)
+    L_ = _pkg().lib()
+    with _allocating(dev, stream):
+        for n in ("dq", "dk") + (("dwq",) if wq is not None else ()) + (("dwk",) if wk is not None else ()):
+            if n not in o:
+                o[n] = torch.empty(kinds[n][1], dtype=kinds[n][0], device=dev)
+        need = L_.ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, code) if "dwq" in o or "dwk" in o else 0
+        ws, pw, nw = _workspace(where, workspace, need, dev)
+    dwq, dwk = o.get("dwq"), o.get("dwk")
+    _done(L_.ssm_qk_rope_bwd(*head, pp, eps, pdq, pdk, o["dq"].data_ptr(), o["dk"].data_ptr(),
+                             None if dwq is None else dwq.data_ptr(), None if dwk is None else dwk.data_ptr(), Bs, L,
+                             Hq, Hk, D, R, code, pw, nw, _raw_stream(dev, stream)), where)
+    return o
+
+
+def ssm_qk_rope_append(q, k, v, wq, wk, freq, pos, k_cache, v_cache, sinks, eps=1e-6, q_out=None, stream=None):
+    """Appends the L new tokens of every row to a window cache: k normed and
+    turned, v as it is; returns q normed and turned (Bs, L, Hq, D). pos (Bs,)
+    int32 is the position of each row's first new token (negative: the row is
+    inactive). k_cache and v_cache (Bs, Hk, sinks + window, D) are written in
+    place: position p < sinks in slot p, else in slot sinks + (p - sinks) %
+    window."""
+    import torch
+    where = "ssm_qk_rope_append"
+    (Bs, L, Hq, Hk, D, R), code, (pq, sq, pk, sk, *rest), eps = _rope_args(where, q, k, wq, wk, freq, eps)
+    dt, dev = q.dtype, q.device
+    pv, sv = _strided(where, "v", v, dt, (Bs, L, Hk, D), dev)
+    pp = _dense(where, "pos", pos, torch.int32, (Bs,), dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("%s: k_cache must be a 4-D tensor (Bs, Hk, sinks + window, D)" % where)
+    C = k_cache.shape[2]
+    sinks = int(sinks)
+    if not 0 <= sinks < C:
+        raise ValueError("%s: sinks must lie in [0, %d) for a cache of %d slots, got %d" % (where, C, C, sinks))
+    pkc = _dense(where, "k_cache", k_cache, dt, (Bs, Hk, C, D), dev)
+    pvc = _dense(where, "v_cache", v_cache, dt, (Bs, Hk, C, D), dev)
+    pqo = _maybe(where, "q_out", q_out, dt, (Bs, L, Hq, D), dev)
+    _gpu(where, q)
+    if q_out is None:
+        with _allocating(dev, stream):
+            q_out = torch.empty((Bs, L, Hq, D), dtype=dt, device=dev)
+        pqo = q_out.data_ptr()
+    _done(_pkg().lib().ssm_qk_rope_append(pq, sq, pk, sk, pv, sv, *rest, pp, eps, pqo, pkc, pvc, Bs, L, Hq, Hk, D, R,
+                                          C - sinks, sinks, code, _raw_stream(dev, stream)), where)
+    return q_out

@@ -109,3 +109,61 @@ def glr_reference(x, gr, gi, A, h0=None, dy=None, dh_last=None, **_):
     e_dA = e_dlr.sum((0, 1)) + EPS * min(terms, 600) * dlr.abs().sum((0, 1))
     out.update(dx=(dx, e_dx), dgr=(dgr, e_dgr), dgi=(dgi, e_dgi), dA=(dA, e_dA), dh0=(G, eG))
     return out
+
+
+# ---------------------------------------------------------------------------
+# norm and rotation of queries and keys
+# ---------------------------------------------------------------------------
+def rope_inputs(Bs, L, Hq, Hk, D, R, dtype, seed, far=0):
+    """q, k and v are slices of one packed tensor."""
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g)
+    packed = r(Bs, L, Hq + 2 * Hk, D).to(dtype)
+    pos = torch.randint(0, far + 1, (Bs, 1), generator=g, dtype=torch.int32) + torch.arange(L, dtype=torch.int32)
+    return dict(q=packed[:, :, :Hq], k=packed[:, :, Hq:Hq + Hk], v=packed[:, :, Hq + Hk:], wq=r(D), wk=r(D),
+                freq=10000.0 ** (-torch.arange(0, R, 2, dtype=torch.float64) / max(R, 1)), pos=pos,
+                dq_out=r(Bs, L, Hq, D).to(dtype), dk_out=r(Bs, L, Hk, D).to(dtype))
+
+
+def rope_turn(n, pos, freq, back=False):
+    R = 2 * freq.numel()
+    at = (pos.double().unsqueeze(-1) * freq).unsqueeze(2)
+    c, s = at.cos(), at.sin() * (-1 if back else 1)
+    a, b = n[..., :R // 2], n[..., R // 2:R]
+    return torch.cat([a * c - b * s, b * c + a * s, n[..., R:]], -1)
+
+
+def rope_reference(x, w, pos, freq, eps, d=None):
+    """((value, error), and with d the gradients (dx, error), (dw, error)).
+
+    The mean of squares sums D terms (a butterfly: 8 + 5 roundings), the root
+    halves it and adds two; two products: 11 roundings to n. The angle: its
+    fraction of a turn is rounded to float32 (half a turn at most: 2 pi EPS / 2
+    absolute), the double product is off by 2^-52 of the turns; sine and
+    cosine are within 2 EPS: 8 EPS absolute, plus three roundings in the turn."""
+    x = x.double()
+    w = torch.ones(x.shape[-1], dtype=torch.float64) if w is None else w.double()
+    inv = 1 / (x.square().mean(-1, keepdim=True) + eps).sqrt()
+    u = x * inv
+    turns = 2.0 ** -51 * float(pos.abs().max()) if pos.numel() else 0.0
+
+    def size(v):  # of a pair, for the errors of its turned values
+        R = 2 * freq.numel()
+        a, b = v[..., :R // 2].abs(), v[..., R // 2:R].abs()
+        return torch.cat([a + b, a + b, v[..., R:].abs()], -1)
+
+    value = rope_turn(u * w, pos, freq)
+    err = size(u * w) * (22 * EPS + turns)
+    if d is None:
+        return value, err
+    d = d.double()
+    dn, e_dn = rope_turn(d, pos, freq, back=True), size(d) * (11 * EPS + turns)
+    t = dn * w
+    m = (t * u).mean(-1, keepdim=True)
+    e_t = e_dn * w.abs() + EPS * t.abs()
+    e_m = (e_t * u.abs() + 24 * EPS * (t * u).abs()).mean(-1, keepdim=True)
+    dx = inv * (t - u * m)
+    e_dx = inv * (e_t + u.abs() * e_m + (u * m).abs() * 12 * EPS + (t - u * m).abs() * 12 * EPS)
+    dw, terms = (dn * u).sum((0, 1, 2)), x[..., 0].numel()
+    e_dw = (e_dn * u.abs() + 11 * EPS * (dn * u).abs()).sum((0, 1, 2)) + EPS * min(terms, 1000) * (dn * u).abs().sum((0, 1, 2))
+    return (value, err), (dx, e_dx), (dw, e_dw)

@@ -9,7 +9,7 @@ import torch
 
 import state_space_model_selective_amd as ssm
 from state_space_model_selective_amd import hybrid
-from hybrid_util import glr_inputs, glr_reference
+from hybrid_util import glr_inputs, glr_reference, rope_inputs, rope_reference
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ssm_hybrid.h")
 f32, bf16 = torch.float32, torch.bfloat16
@@ -163,3 +163,105 @@ def test_glr_reference_gradient():
     ref = glr_reference(**t)
     for n, g in zip(names, grads):
         assert torch.allclose(ref["d" + n][0], g, rtol=1e-9, atol=1e-11), n
+
+
+# --- norm and rotation -------------------------------------------------------
+def rope(dtype=f32):
+    t = rope_inputs(2, 5, 4, 2, 64, 32, dtype, seed=0)
+    return {n: t[n] for n in ("q", "k", "wq", "wk", "freq")}, t
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_rope_valid_arguments_reach_the_gpu_check(dtype):
+    a, t = rope(dtype)
+    gpu_only(ssm.ssm_qk_rope_fwd, **a, pos=t["pos"], q_out=torch.empty(2, 5, 4, 64, dtype=dtype))
+    gpu_only(ssm.ssm_qk_rope_bwd, **a, dq_out=t["dq_out"], dk_out=t["dk_out"], out={"dwq": torch.empty(64)})
+    c = torch.zeros(2, 2, 20, 64, dtype=dtype)
+    gpu_only(ssm.ssm_qk_rope_append, **a, v=t["v"], pos=t["pos"][:, 0].contiguous(), k_cache=c, v_cache=c.clone(), sinks=4)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", torch.zeros(2, 5, 4, 64, dtype=torch.float16)), ("q", torch.zeros(2, 5, 256)), ("k", torch.zeros(2, 6, 2, 64)),
+    ("k", torch.zeros(2, 5, 2, 64, dtype=bf16)), ("k", torch.zeros(2, 5, 64)), ("k", torch.zeros(2, 5, 64, 2).transpose(2, 3)),
+    ("wq", torch.zeros(63)), ("wk", torch.zeros(64, dtype=bf16)), ("freq", torch.zeros(16)),
+    ("freq", torch.zeros(4, 4, dtype=torch.float64)), ("pos", torch.zeros(2, 5, dtype=torch.int64)),
+    ("pos", torch.zeros(5, dtype=torch.int32)), ("q_out", torch.zeros(2, 5, 4, 128)[..., :64]),
+    ("k_out", torch.zeros(2, 5, 2, 64, dtype=bf16)), ("wq", torch.zeros(64, device="meta"))])
+def test_rope_refusals(name, bad):
+    a, _ = rope()
+    a[name] = bad
+    refuses(name, ssm.ssm_qk_rope_fwd, **a)
+
+
+def test_rope_backward_and_append_refusals():
+    a, t = rope()
+    refuses("dq_out", ssm.ssm_qk_rope_bwd, **a, dq_out=None, dk_out=t["dk_out"])
+    refuses("dk_out", ssm.ssm_qk_rope_bwd, **a, dq_out=t["dq_out"], dk_out=t["dk_out"][:, :4])
+    refuses("unknown output", ssm.ssm_qk_rope_bwd, **a, dq_out=t["dq_out"], dk_out=t["dk_out"], out={"dv": t["v"]})
+    c, pos = torch.zeros(2, 2, 20, 64), t["pos"][:, 0].contiguous()
+    ok = dict(a, v=t["v"], pos=pos, k_cache=c, v_cache=c.clone(), sinks=4)
+    for name, bad, says in (("v", t["v"][:, :4], "v"), ("pos", None, "pos"), ("pos", t["pos"], "pos"), ("sinks", 20, "sinks"),
+                            ("sinks", -1, "sinks"), ("k_cache", c[0], "k_cache"), ("v_cache", c[:, :, :10], "v_cache"),
+                            ("k_cache", torch.zeros(2, 3, 20, 64), "k_cache")):
+        refuses(says, ssm.ssm_qk_rope_append, **dict(ok, **{name: bad}))
+
+
+def c_rope(fn, **kw):
+    v = dict(q=P[0], qs=None, k=P[1], ks=None, v=P[2], vs=None, wq=P[3], wk=P[4], freq=P[5], pos=P[6], eps=1e-6, qo=P[7],
+             ko=P[8], dqo=P[9], dko=P[10], dwq=P[11], dwk=P[12], Bs=2, L=8, Hq=4, Hk=2, D=64, R=64, window=16, sinks=4,
+             dt=0, ws=P[13], wb=1 << 30)
+    v.update(kw)
+    names = {"ssm_qk_rope_fwd": "q qs k ks wq wk freq pos eps qo ko Bs L Hq Hk D R dt",
+             "ssm_qk_rope_bwd": "q qs k ks wq wk freq pos eps dqo dko qo ko dwq dwk Bs L Hq Hk D R dt ws wb",
+             "ssm_qk_rope_append": "q qs k ks v vs wq wk freq pos eps qo ko dko Bs L Hq Hk D R window sinks dt"}[fn]
+    args = [ctypes.byref(v[n]) if isinstance(v[n], ctypes.Structure) else v[n] for n in names.split()]
+    return getattr(ssm.lib(), fn)(*args, None)
+
+
+@host_only
+@pytest.mark.parametrize("fn", ["ssm_qk_rope_fwd", "ssm_qk_rope_bwd", "ssm_qk_rope_append"])
+def test_rope_abi_refusals(fn):
+    call = lambda **kw: c_rope(fn, **kw)
+    for n in ("q", "k", "freq", "qo", "ko"):
+        assert call(**{n: None}) == ssm.SSM_ERR_NULL, n
+    for n in ("q", "wq", "pos", "freq", "ko"):
+        assert call(**{n: P[20] + 8}) == ssm.SSM_ERR_UNSUPPORTED, n
+    for n in ("Bs", "L", "Hq", "Hk"):
+        assert call(**{n: -1}) == ssm.SSM_ERR_DIM, n
+    assert call(Bs=1 << 40, L=1 << 20) == ssm.SSM_ERR_DIM
+    for kw in (dict(D=96), dict(D=32, R=16), dict(R=8), dict(R=80), dict(dt=3)):
+        assert call(**kw) == ssm.SSM_ERR_UNSUPPORTED, kw
+    assert call(eps=-1.0) == ssm.SSM_ERR_ARG and call(eps=float("nan")) == ssm.SSM_ERR_ARG
+    S = hybrid.SSMStrides
+    assert call(qs=S(2048, 256, 66)) == ssm.SSM_ERR_UNSUPPORTED
+    assert call(qs=S(-2048, 256, 64)) == ssm.SSM_ERR_UNSUPPORTED
+    assert call(ks=S(1 << 60, 256, 64), Bs=1 << 20) == ssm.SSM_ERR_DIM
+    assert call(qo=P[0]) == ssm.SSM_ERR_ALIAS and call(ko=P[7]) == ssm.SSM_ERR_ALIAS
+    assert call(qs=S(1 << 29, 256, 64), Bs=2) == ssm.SSM_ERR_ALIAS  # the rows span other buffers
+    none = dict(q=None, k=None, v=None, pos=None, qo=None, ko=None, dqo=None, dko=None, freq=None, dwq=None, dwk=None)
+    assert call(**dict(none, Bs=0)) == ssm.SSM_OK
+
+
+@host_only
+def test_rope_abi_refusals_of_one():
+    assert c_rope("ssm_qk_rope_bwd", ws=None) == ssm.SSM_ERR_WORKSPACE
+    assert c_rope("ssm_qk_rope_bwd", wb=64) == ssm.SSM_ERR_WORKSPACE
+    assert c_rope("ssm_qk_rope_bwd", dqo=None) == ssm.SSM_ERR_NULL
+    assert c_rope("ssm_qk_rope_bwd", dwk=P[11]) == ssm.SSM_ERR_ALIAS
+    for kw in (dict(window=0), dict(sinks=-1), dict(window=1 << 31), dict(window=1 << 30, sinks=1 << 30)):
+        assert c_rope("ssm_qk_rope_append", **kw) == ssm.SSM_ERR_DIM
+    for n in ("v", "pos", "dko"):
+        assert c_rope("ssm_qk_rope_append", **{n: None}) == ssm.SSM_ERR_NULL
+    assert c_rope("ssm_qk_rope_append", vs=hybrid.SSMStrides(512, 128, 2)) == ssm.SSM_ERR_UNSUPPORTED
+
+
+def test_rope_reference_gradient():
+    t = {n: v.double() for n, v in rope_inputs(2, 4, 3, 1, 64, 32, f32, seed=1).items()}
+    q, w = t["q"].clone().requires_grad_(), t["wq"].clone().requires_grad_()
+    n = q / (q.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w
+    at = (t["pos"].unsqueeze(-1) * t["freq"]).unsqueeze(2)
+    z = torch.complex(n[..., :16], n[..., 16:32]) * torch.polar(torch.ones_like(at), at)
+    loss = (torch.cat([z.real, z.imag, n[..., 32:]], -1) * t["dq_out"]).sum()
+    dq, dw = torch.autograd.grad(loss, (q, w))
+    _, dx, dwr = rope_reference(t["q"], t["wq"], t["pos"], t["freq"], 1e-6, t["dq_out"])
+    assert torch.allclose(dx[0], dq, rtol=1e-9, atol=1e-12) and torch.allclose(dwr[0], dw, rtol=1e-9, atol=1e-12)
