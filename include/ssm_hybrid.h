@@ -12,7 +12,8 @@
  * The conventions of ssm_scan.h hold: device pointers, caller-owned buffers,
  * arguments checked on the host before any HIP call, kernels enqueued on
  * `stream`, ssm_status results, dtype (ssm_dtype) for the tensors said to be
- * "of dtype", float32 sums and states, every pointer aligned to 16 bytes,
+ * "of dtype", float32 sums and states, every pointer aligned to 16 bytes (the
+ * int32 arrays pos and lens to 4, so that they may be parts of longer ones),
  * results that do not depend on timing (repeated calls give identical bits).
  * Empty inputs are valid, and a buffer with no elements may then be NULL.
  *
@@ -146,6 +147,67 @@ int ssm_qk_rope_append(const void* q, const ssm_strides* qs, const void* k, cons
                        const int32_t* pos, double eps, void* q_out, void* k_cache, void* v_cache, int64_t Bs,
                        int64_t L, int64_t Hq, int64_t Hk, int64_t D, int64_t R, int64_t window, int64_t sinks,
                        int dtype, void* stream);
+
+/*
+ * Attention with a sliding window and sinks. Query i of Lq stands at position
+ * i + Lk - Lq of its row's Lk keys (the queries are the last Lq positions; with
+ * Lq > Lk the first ones stand before every key). At position p it sees key j
+ * when
+ *
+ *   j <= p   and   j < lens[b] (Lk if lens is NULL)   and   (p - j < window or j < sinks)
+ *
+ *   s_ij = scale q_i . k_j,   o_i = sum_j softmax_j(s_ij) v_j over the keys it sees
+ *
+ * and gives zeros (lse -inf) when it sees none. What an unseen key or value
+ * holds does not matter, be it infinite or NaN. Head h of q goes with head
+ * h / (Hq / Hk) of k and v.
+ *   q    : (Bs, Lq, Hq, D) of dtype, strided by qs
+ *   k, v : (Bs, Lk, Hk, D) of dtype, strided by ks, vs
+ *   lens : (Bs) int32, or NULL; values are clamped to [0, Lk]
+ *   o    : (Bs, Lq, Hq, D) of dtype, dense
+ *   lse  : (Bs, Hq, Lq) float32, or NULL -- log sum_j exp(s_ij), for ssm_swa_bwd
+ * Supported: D 64 or 128, Hq a multiple of Hk >= 1, window >= 1, sinks >= 0,
+ * Lq and Lk up to 2^30 (else SSM_ERR_DIM), token strides up to 32 MiB, scale
+ * positive and finite (else SSM_ERR_ARG). The softmax and every sum are
+ * float32. With float32 inputs the products are float32; with bfloat16 they
+ * run on the bf16 matrix instructions, the weights (and in the backward their
+ * gradients) rounded to nearest even on the way into the second product, each
+ * within 2^-9 of its value; lse sums the unrounded weights.
+ */
+int ssm_swa_fwd(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks, const void* v,
+                const ssm_strides* vs, const int32_t* lens, double scale, void* o, float* lse, int64_t Bs, int64_t Lq,
+                int64_t Lk, int64_t Hq, int64_t Hk, int64_t D, int64_t window, int64_t sinks, int dtype, void* stream);
+
+/*
+ * Backward pass: from o and lse as ssm_swa_fwd wrote them for the same
+ * arguments and dout, the gradient of o (both dense), the gradients dq (Bs,
+ * Lq, Hq, D), dk and dv (Bs, Lk, Hk, D) of dtype, dense, written in full. dk
+ * and dv sum over the queries of all heads that share them in a fixed order.
+ * workspace: ssm_swa_bwd_workspace_bytes(), no initialisation needed.
+ */
+size_t ssm_swa_bwd_workspace_bytes(int64_t Bs, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hk, int64_t D,
+                                   int64_t sinks, int dtype);
+int ssm_swa_bwd(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks, const void* v,
+                const ssm_strides* vs, const int32_t* lens, double scale, const void* o, const float* lse,
+                const void* dout, void* dq, void* dk, void* dv, int64_t Bs, int64_t Lq, int64_t Lk, int64_t Hq,
+                int64_t Hk, int64_t D, int64_t window, int64_t sinks, int dtype, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * One token of every row over a window cache (ssm_qk_rope_append): row b's
+ * query sees the min(pos[b] + 1, C) slots that are filled when the token at
+ * position pos[b] has been appended. pos[b] < 0: an inactive row, zeros.
+ *   q : (Bs, Hq, D) of dtype; its strides are those of qs for (batch, head),
+ *       qs->token is not used
+ *   k_cache, v_cache : (Bs, Hk, C, D) of dtype, dense;  pos : (Bs) int32
+ *   o : (Bs, Hq, D) of dtype, dense
+ *   workspace : ssm_swa_decode_workspace_bytes(), no initialisation needed;
+ *               NULL when that is zero
+ */
+size_t ssm_swa_decode_workspace_bytes(int64_t Bs, int64_t C, int64_t Hq, int64_t Hk, int64_t D, int dtype);
+int ssm_swa_decode(const void* q, const ssm_strides* qs, const void* k_cache, const void* v_cache, const int32_t* pos,
+                   double scale, void* o, int64_t Bs, int64_t C, int64_t Hq, int64_t Hk, int64_t D, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

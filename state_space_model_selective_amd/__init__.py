@@ -15,13 +15,14 @@ import subprocess
 
 from .hybrid import (PROTOTYPES as _HYBRID_PROTOTYPES, ssm_glr_bwd, ssm_glr_bwd_workspace_bytes, ssm_glr_ckpt_shape,
                      ssm_glr_fwd, ssm_glr_step, ssm_glr_workspace_bytes, ssm_qk_rope_append, ssm_qk_rope_bwd,
-                     ssm_qk_rope_bwd_workspace_bytes, ssm_qk_rope_fwd)
+                     ssm_qk_rope_bwd_workspace_bytes, ssm_qk_rope_fwd, ssm_swa_bwd, ssm_swa_bwd_workspace_bytes,
+                     ssm_swa_decode, ssm_swa_decode_workspace_bytes, ssm_swa_fwd)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "libssm_scan.so")
 SOURCES = [os.path.join(_HERE, "csrc", n) for n in ("ssm_scan.hip", "ssm_scan_bwd.hip", "ssm_ssd.hip",
-                                                    "ssm_glr.hip", "ssm_qk_rope.hip")]
+                                                    "ssm_glr.hip", "ssm_qk_rope.hip", "ssm_swa.hip", "ssm_swa_decode.hip")]
 # issue-rate probe of the vector ALU (measurement only; used by the benchmark's --micro mode)
 PROBE_LIB_PATH = os.path.join(_HERE, "libssm_valu_probe.so")
 PROBE_SOURCES = [os.path.join(_HERE, "csrc", "valu_probe.hip")]

@@ -76,6 +76,7 @@ struct Buf {
   const void* p;
   int64_t bytes;
   bool required, out;
+  unsigned align = 16;
 };
 
 // Null, alignment and overlap of the buffers of one call (an output overlaps
@@ -84,7 +85,7 @@ int check_bufs(const Buf* v, int n) {
   for (int i = 0; i < n; ++i)
     if (v[i].required && v[i].bytes > 0 && !v[i].p) return SSM_ERR_NULL;
   for (int i = 0; i < n; ++i)
-    if (v[i].p && !aligned16(v[i].p)) return SSM_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(v[i].p) % v[i].align) return SSM_ERR_UNSUPPORTED;
   for (int i = 0; i < n; ++i)
     for (int j = 0; j < n; ++j)
       if (i != j && v[i].out && v[i].p && v[j].p && v[i].bytes > 0 && v[j].bytes > 0 &&

@@ -318,7 +318,7 @@ extern "C" int ssm_qk_rope_fwd(const void* q, const ssm_strides* qs, const void*
   if ((rc = strided(ks, Bs, L, Hk, D, es, &sk, &bk)) != SSM_OK) return rc;
   const int64_t any = nq + nk > 0;
   const Buf bufs[] = {{q, bq, true, false},       {k, bk, true, false},          {wq, D * 4, false, false},
-                      {wk, D * 4, false, false},  {freq, any * R * 4, true, false}, {pos, any * Bs * L * 4, false, false},
+                      {wk, D * 4, false, false},  {freq, any * R * 4, true, false}, {pos, any * Bs * L * 4, false, false, 4},
                       {q_out, nq * es, true, true}, {k_out, nk * es, true, true}};
   if ((rc = check_bufs(bufs, 8)) != SSM_OK) return rc;
   if (!any) return SSM_OK;
@@ -356,7 +356,7 @@ extern "C" int ssm_qk_rope_bwd(const void* q, const ssm_strides* qs, const void*
   const bool weights = dwq || dwk;
   const size_t need = weights ? ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, dtype) : 0;
   const Buf bufs[] = {{q, bq, true, false},        {k, bk, true, false},           {wq, D * 4, false, false},
-                      {wk, D * 4, false, false},   {freq, any * R * 4, true, false}, {pos, any * Bs * L * 4, false, false},
+                      {wk, D * 4, false, false},   {freq, any * R * 4, true, false}, {pos, any * Bs * L * 4, false, false, 4},
                       {dq_out, nq * es, true, false}, {dk_out, nk * es, true, false}, {dq, nq * es, true, true},
                       {dk, nk * es, true, true},   {dwq, D * 4, false, true},      {dwk, D * 4, false, true},
                       {workspace, static_cast<int64_t>(need), false, true}};
@@ -394,7 +394,7 @@ extern "C" int ssm_qk_rope_append(const void* q, const ssm_strides* qs, const vo
   const int64_t any = nq + nk > 0;
   const Buf bufs[] = {{q, bq, true, false},      {k, bk, true, false},           {v, bv, true, false},
                       {wq, D * 4, false, false}, {wk, D * 4, false, false},      {freq, any * R * 4, true, false},
-                      {pos, any * Bs * 4, true, false}, {q_out, nq * es, true, true}, {k_cache, any * bc, true, true},
+                      {pos, any * Bs * 4, true, false, 4}, {q_out, nq * es, true, true}, {k_cache, any * bc, true, true},
                       {v_cache, any * bc, true, true}};
   if ((rc = check_bufs(bufs, 10)) != SSM_OK) return rc;
   if (!any) return SSM_OK;

@@ -1,0 +1,222 @@
+// Attention of single tokens over a window cache (ssm_swa_decode of
+// ssm_hybrid.h) for gfx950.
+//
+// Every filled slot is seen, so a row's keys are simply the first n = min(pos
+// + 1, C) slots. The heads that share keys are the columns of one matrix
+// product with 32 keys (column padding costs nothing here: the cache's bytes
+// bound the call). A row's tiles of 32 keys are shared by `nsplit` workgroups
+// and their waves; each wave keeps its own maximum, sum and weighted values,
+// which are joined in a fixed order, over the waves through LDS and over the
+// workgroups by a second kernel.
+#include "swa_common.h"
+
+namespace {
+
+constexpr int kWaves = 4;
+
+template <typename T>
+struct DecodeArgs {
+  const T* q;
+  const T* kc;
+  const T* vc;
+  const int32_t* pos;
+  T* o;
+  float* part;  // (Bs, Hk, GB, nsplit, 32): D values, maximum, sum
+  int64_t q_batch, q_head;
+  int64_t C;
+  int Bs, Hq, Hk, G, GB, nsplit;  // GB: blocks of 32 heads of a group
+  float scale;
+};
+
+// a column's record: D values, the maximum, the sum (and padding to 16 bytes)
+template <int D>
+constexpr int kRecord = D + 4;
+
+template <typename T, int D>
+__global__ __launch_bounds__(64 * kWaves, 1) void swa_decode_kernel(const DecodeArgs<T> p) {
+  constexpr int KK = D / 16, DB = D / 32, R = kRecord<D>;
+  using KT = Tile<T, D, 32>;
+  // a wave's key and value tile, afterwards its record of every column
+  constexpr int kOwn = 2 * KT::kBytes > 32 * R * 4 ? 2 * KT::kBytes : 32 * R * 4;
+  __shared__ __attribute__((aligned(16))) char sm[kWaves][kOwn];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 31, hi = lane >> 5;
+  int w = blockIdx.x;
+  const int split = w % p.nsplit;
+  w /= p.nsplit;
+  const int gb = w % p.GB;
+  w /= p.GB;
+  const int hk = w % p.Hk, b = w / p.Hk;
+  int64_t held = static_cast<int64_t>(p.pos[b]) + 1;
+  held = held < 0 ? 0 : held > p.C ? p.C : held;
+  const int64_t tiles = (held + 31) / 32;
+  const int64_t t0 = tiles * split / p.nsplit, t1 = tiles * (split + 1) / p.nsplit;
+  const int g = 32 * gb + n, gc = g < p.G ? g : p.G - 1;
+  const T* kbase = p.kc + (static_cast<int64_t>(b) * p.Hk + hk) * p.C * D;
+  const T* vbase = p.vc + (static_cast<int64_t>(b) * p.Hk + hk) * p.C * D;
+  const T* qr = p.q + b * p.q_batch + (hk * static_cast<int64_t>(p.G) + gc) * p.q_head;
+  Frag<T> q[KK];
+#pragma unroll
+  for (int kk = 0; kk < KK; ++kk) q[kk] = load_frag(qr + 16 * kk + 8 * hi);
+  const float sc = p.scale * kLog2e;
+  float top = -INFINITY, l = 0.f;
+  v16f o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) o[d] = v16f{};
+  for (int64_t t = t0 + wave; t < t1; t += kWaves) {
+    const T* kt = kbase + t * 32 * D;
+    const T* vt = vbase + t * 32 * D;
+    const int last = static_cast<int>(held - 1 - t * 32 < 31 ? held - 1 - t * 32 : 31);
+    KT::template load<64>(kt, D, 0, last, sm[wave], 0, lane);
+    KT::template load<64>(vt, D, 0, last, sm[wave] + KT::kBytes, 0, lane);
+    wait_loads();
+    v16f s = v16f{};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) s = mma(KT::row(sm[wave], n, kk, hi), q[kk], s);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      if (8 * (r >> 2) + 4 * hi + (r & 3) > last) s[r] = -INFINITY;
+      mx = fmaxf(mx, s[r]);
+    }
+    const float now = fmaxf(top, pair_max(mx) * sc);
+    const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - now);
+    const float ref = now == -INFINITY ? 0.f : now;
+    top = now;
+    l *= keep;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -ref));
+      l += s[r];
+    }
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] *= keep;
+    // (the rows past the last one repeat it and have weight 0: a value that is
+    // not finite is one that the query sees)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Frag<T> w8 = as_operand<T>(s, h);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = mma(KT::col(sm[wave] + KT::kBytes, 16 * h, d, lane), w8, o[d]);
+    }
+  }
+  l = pair_sum(l);
+  {
+    float* rec = reinterpret_cast<float*>(sm[wave]) + n * R;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        *reinterpret_cast<float4*>(rec + 32 * d + 8 * r + 4 * hi) =
+            make_float4(o[d][4 * r], o[d][4 * r + 1], o[d][4 * r + 2], o[d][4 * r + 3]);
+    if (hi == 0) rec[D] = top, rec[D + 1] = l;
+  }
+  __syncthreads();
+  // join the waves; D threads a column
+  const int cols = p.G - 32 * gb < 32 ? p.G - 32 * gb : 32;
+  for (int e = threadIdx.x; e < cols * D; e += 64 * kWaves) {
+    const int c = e / D, d = e % D;
+    float m = -INFINITY;
+    for (int x = 0; x < kWaves; ++x) m = fmaxf(m, reinterpret_cast<const float*>(sm[x])[c * R + D]);
+    float sum = 0.f, val = 0.f;
+    for (int x = 0; x < kWaves; ++x) {
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(reinterpret_cast<const float*>(sm[x])[c * R + D] - m);
+      sum = __builtin_fmaf(f, reinterpret_cast<const float*>(sm[x])[c * R + D + 1], sum);
+      val = __builtin_fmaf(f, reinterpret_cast<const float*>(sm[x])[c * R + d], val);
+    }
+    if (p.nsplit == 1) {
+      p.o[(static_cast<int64_t>(b) * p.Hq + hk * p.G + 32 * gb + c) * D + d] = from_f32<T>(sum == 0.f ? 0.f : val / sum);
+    } else {
+      float* out = p.part + (static_cast<int64_t>(blockIdx.x) * 32 + c) * R;
+      out[d] = val;
+      if (d == 0) out[D] = m, out[D + 1] = sum;
+    }
+  }
+}
+
+// One workgroup a head: the join over the splits.
+template <typename T, int D>
+__global__ __launch_bounds__(D) void swa_decode_join_kernel(const DecodeArgs<T> p) {
+  constexpr int R = kRecord<D>;
+  const int head = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq, d = threadIdx.x;
+  const int hk = head / p.G, g = head % p.G;
+  const float* part = p.part + (((static_cast<int64_t>(b) * p.Hk + hk) * p.GB + g / 32) * p.nsplit * 32 + g % 32) * R;
+  float m = -INFINITY;
+  for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, part[static_cast<int64_t>(s) * 32 * R + D]);
+  float sum = 0.f, val = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float* r = part + static_cast<int64_t>(s) * 32 * R;
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r[D] - m);
+    sum = __builtin_fmaf(f, r[D + 1], sum);
+    val = __builtin_fmaf(f, r[d], val);
+  }
+  p.o[(static_cast<int64_t>(b) * p.Hq + head) * D + d] = from_f32<T>(sum == 0.f ? 0.f : val / sum);
+}
+
+// Workgroups that share a row's cache: about two for each compute unit over
+// the whole call, while each of their waves has a tile.
+int decode_splits(int64_t Bs, int64_t C, int64_t Hk, int64_t GB) {
+  const int64_t want = 512 / std::max<int64_t>(1, Bs * Hk * GB);
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, (C + 32 * kWaves - 1) / (32 * kWaves))));
+}
+
+int decode_sizes(int64_t Bs, int64_t C, int64_t Hq, int64_t Hk, int64_t D, double scale, int dtype, int64_t* nq,
+                 int64_t* nc) {
+  int64_t t, bytes;
+  if (C < 0 || C > INT32_MAX || Hk < 1 || Hq < 1 || Hq % Hk || Bs < 0) return SSM_ERR_DIM;
+  if (!mul_nn(Bs, Hq, &t) || t > kMaxGrid || !mul_nn(t, D, nq) || !mul_nn(*nq, 8, &bytes)) return SSM_ERR_DIM;
+  if (!mul_nn(Bs, Hk, &t) || !mul_nn(t, C, &t) || !mul_nn(t, D, nc) || !mul_nn(*nc, 8, &bytes)) return SSM_ERR_DIM;
+  if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return SSM_ERR_UNSUPPORTED;
+  if (!(scale > 0) || scale > 1e30) return SSM_ERR_ARG;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" size_t ssm_swa_decode_workspace_bytes(int64_t Bs, int64_t C, int64_t Hq, int64_t Hk, int64_t D, int dtype) {
+  int64_t nq, nc;
+  if (decode_sizes(Bs, C, Hq, Hk, D, 1.0, dtype, &nq, &nc) != SSM_OK || nq == 0) return 0;
+  const int64_t GB = (Hq / Hk + 31) / 32, n = decode_splits(Bs, C, Hk, GB);
+  return n > 1 ? static_cast<size_t>(Bs * Hk * GB * n * 32 * (D + 4) * 4) : 0;
+}
+
+extern "C" int ssm_swa_decode(const void* q, const ssm_strides* qs, const void* k_cache, const void* v_cache,
+                              const int32_t* pos, double scale, void* o, int64_t Bs, int64_t C, int64_t Hq, int64_t Hk,
+                              int64_t D, int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  int64_t nq, nc, bq;
+  int rc = decode_sizes(Bs, C, Hq, Hk, D, scale, dtype, &nq, &nc);
+  if (rc != SSM_OK) return rc;
+  const int es = dtype == SSM_F32 ? 4 : 2;
+  ssm_strides sq = qs ? *qs : ssm_strides{Hq * D, 0, D};
+  sq.token = 0;
+  if ((rc = strided(&sq, Bs, 1, Hq, D, es, &sq, &bq)) != SSM_OK) return rc;
+  const size_t need = ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, dtype);
+  const Buf bufs[] = {{q, bq, true, false}, {k_cache, nc * es, true, false}, {v_cache, nc * es, true, false},
+                      {pos, Bs * 4, true, false, 4}, {o, nq * es, true, true},
+                      {workspace, static_cast<int64_t>(need), false, true}};
+  if ((rc = check_bufs(bufs, 6)) != SSM_OK) return rc;
+  if (nq == 0) return SSM_OK;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  auto go = [&](auto tag, auto dim) {
+    using T = decltype(tag);
+    constexpr int DD = decltype(dim)::value;
+    DecodeArgs<T> a{};
+    a.q = static_cast<const T*>(q), a.kc = static_cast<const T*>(k_cache), a.vc = static_cast<const T*>(v_cache);
+    a.pos = pos, a.o = static_cast<T*>(o), a.part = static_cast<float*>(workspace);
+    a.q_batch = sq.batch, a.q_head = sq.head, a.C = C;
+    a.Bs = static_cast<int>(Bs), a.Hq = static_cast<int>(Hq), a.Hk = static_cast<int>(Hk);
+    a.G = static_cast<int>(Hq / Hk), a.GB = (a.G + 31) / 32, a.nsplit = decode_splits(Bs, C, Hk, a.GB);
+    a.scale = static_cast<float>(scale);
+    const unsigned grid = static_cast<unsigned>(Bs * Hk * a.GB * a.nsplit);
+    hipLaunchKernelGGL((swa_decode_kernel<T, DD>), dim3(grid), dim3(64 * kWaves), 0, st, a);
+    if (a.nsplit > 1)
+      hipLaunchKernelGGL((swa_decode_join_kernel<T, DD>), dim3(static_cast<unsigned>(Bs * Hq)), dim3(DD), 0, st, a);
+    return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == SSM_F32) return D == 64 ? go(float{}, D64{}) : go(float{}, D128{});
+  return D == 64 ? go(uint16_t{}, D64{}) : go(uint16_t{}, D128{});
+}

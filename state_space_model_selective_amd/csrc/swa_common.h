@@ -1,0 +1,269 @@
+// Internal helpers of the sliding-window attention kernels: operands of the
+// 32x32 matrix instructions, LDS tiles, the mask (not part of the public C ABI).
+//
+// Every product has 32x32 result tiles and contracts 16 entries at a time. A
+// lane (m = lane % 32, hi = lane / 32) gives 8 entries of operand row m (A)
+// or column m (B) and holds 16 results of column m, register r being row
+// 8 (r / 4) + 4 hi + r % 4. An operand read along rows ("row operand") has
+// the entries 8 hi + 0..7; one read across rows ("column operand", of the
+// transpose) has the rows 4 hi + 0..3 and 8 + 4 hi + 0..3, which are the rows
+// that result registers 8 s .. 8 s + 7 hold of the contraction's step s: so
+// a result tile is the other operand of the next product as it stands, and
+// neither the weights nor their gradients leave the registers.
+// bfloat16: one 32x32x16 instruction a step; float32: eight 32x32x2.
+#ifndef SSM_SWA_COMMON_H
+#define SSM_SWA_COMMON_H
+
+#include "hybrid_common.h"
+
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+
+template <typename T>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+  uint4 v;
+};
+template <>
+struct Frag<float> {
+  float v[8];
+};
+
+__device__ __forceinline__ v16f mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, v16f c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a.v), __builtin_bit_cast(v8bf, b.v), c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mma(const Frag<float>& a, const Frag<float>& b, v16f c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a.v[j], b.v[j], c, 0, 0, 0);
+  return c;
+}
+
+// Result registers 8 s .. 8 s + 7 as an operand (bfloat16: rounded to nearest
+// even; the sums they enter are float32).
+template <typename T>
+__device__ __forceinline__ Frag<T> as_operand(const v16f& x, int s) {
+  Frag<T> f;
+  if constexpr (sizeof(T) == 2) {
+    f.v = make_uint4(pack_bf16(x[8 * s], x[8 * s + 1]), pack_bf16(x[8 * s + 2], x[8 * s + 3]),
+                     pack_bf16(x[8 * s + 4], x[8 * s + 5]), pack_bf16(x[8 * s + 6], x[8 * s + 7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f.v[j] = x[8 * s + j];
+  }
+  return f;
+}
+
+// 8 consecutive entries from global memory.
+__device__ __forceinline__ Frag<uint16_t> load_frag(const uint16_t* p) {
+  return Frag<uint16_t>{*reinterpret_cast<const uint4*>(p)};
+}
+__device__ __forceinline__ Frag<float> load_frag(const float* p) {
+  Frag<float> f;
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  f.v[0] = a.x, f.v[1] = a.y, f.v[2] = a.z, f.v[3] = a.w, f.v[4] = b.x, f.v[5] = b.y, f.v[6] = b.z, f.v[7] = b.w;
+  return f;
+}
+__device__ __forceinline__ float frag_dot(const Frag<uint16_t>& a, const Frag<uint16_t>& b) {
+  float x[8], y[8], s = 0.f;
+  Vec16<uint16_t>::widen(a.v, x);
+  Vec16<uint16_t>::widen(b.v, y);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = __builtin_fmaf(x[j], y[j], s);
+  return s;
+}
+__device__ __forceinline__ float frag_dot(const Frag<float>& a, const Frag<float>& b) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s = __builtin_fmaf(a.v[j], b.v[j], s);
+  return s;
+}
+
+// v combined over the two lanes that share a column (v_permlane32_swap).
+__device__ __forceinline__ float pair_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------------------
+// An LDS tile of ROWS rows of D entries, in 16-byte chunks. Chunk c of row r
+// lies at position c ^ swizzle(r) of its row, so that 16 lanes on 16 rows
+// (row operand) and the lanes of a transposing read on 4 rows (column
+// operand) each touch every bank once. The tile is written by loads that go
+// from global memory to LDS directly: their LDS addresses are consecutive, so
+// the lane picks the global chunk.
+// ---------------------------------------------------------------------------
+template <typename T, int D, int ROWS>
+struct Tile {
+  static constexpr int kCpr = D * static_cast<int>(sizeof(T)) / 16;  // chunks of a row
+  static constexpr int kBytes = ROWS * kCpr * 16;
+
+  static __device__ __forceinline__ int swizzle(int r) {
+    if constexpr (kCpr == 8) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int r, int c) { return (r * kCpr + (c ^ swizzle(r))) * 16; }
+
+  // Rows row0 .. row0 + ROWS - 1 (those past `last` read row `last` instead,
+  // so that no row outside the valid ones is ever read; last >= row0). Each of
+  // the workgroup's NT threads moves chunks; the caller waits for vmcnt(0).
+  template <int NT>
+  static __device__ __forceinline__ void load(const T* base, int64_t stride, int row0, int last, char* lds, int wave,
+                                              int lane) {
+    static_assert(ROWS * kCpr % NT == 0, "whole passes");
+    const char* first = reinterpret_cast<const char*>(base + row0 * stride);
+    const unsigned row_bytes = static_cast<unsigned>(stride * static_cast<int64_t>(sizeof(T)));
+#pragma unroll
+    for (int it = 0; it < ROWS * kCpr / NT; ++it) {
+      const int id = it * NT + wave * 64 + lane;
+      const int r = id / kCpr, c = (id % kCpr) ^ swizzle(r);
+      const int rr = row0 + r <= last ? r : last - row0;
+      const unsigned off = static_cast<unsigned>(rr) * row_bytes + static_cast<unsigned>(c) * 16u;
+      char* dst = lds + (it * NT + wave * 64) * 16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(first + off),
+                                       (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
+    }
+  }
+
+  // Row operand: entries 16 kk + 8 hi + 0..7 of row r.
+  static __device__ __forceinline__ Frag<T> row(const char* lds, int r, int kk, int hi) {
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+      f.v = *reinterpret_cast<const uint4*>(lds + at(r, 2 * kk + hi));
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(lds + at(r, 4 * kk + 2 * hi));
+      const float4 b = *reinterpret_cast<const float4*>(lds + at(r, 4 * kk + 2 * hi + 1));
+      f.v[0] = a.x, f.v[1] = a.y, f.v[2] = a.z, f.v[3] = a.w, f.v[4] = b.x, f.v[5] = b.y, f.v[6] = b.z, f.v[7] = b.w;
+    }
+    return f;
+  }
+
+  // Column operand: column 32 db + lane % 32 of rows r0 + 4 hi + 0..3 and
+  // r0 + 8 + 4 hi + 0..3 (bfloat16: two transposing reads, in which the 16
+  // lanes of a group name 4 rows x 16 columns and each receives a column).
+  static __device__ __forceinline__ Frag<T> col(const char* lds, int r0, int db, int lane) {
+    const int hi = lane >> 5;
+    Frag<T> f;
+    if constexpr (sizeof(T) == 2) {
+      const int i = lane & 15, c = 32 * db + (lane & 16) + 4 * (i & 3), r = r0 + 4 * hi + (i >> 2);
+      typedef __attribute__((address_space(3))) v4s* Ptr;
+      const uint2 a = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(const_cast<char*>(lds) + at(r, c >> 3) + (c & 7) * 2)));
+      const uint2 b = __builtin_bit_cast(
+          uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((Ptr)(const_cast<char*>(lds) + at(r + 8, c >> 3) + (c & 7) * 2)));
+      f.v = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      const int c = 32 * db + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = r0 + 4 * hi + (j & 3) + 8 * (j >> 2);
+        f.v[j] = *reinterpret_cast<const float*>(lds + at(r, c >> 2) + (c & 3) * 4);
+      }
+    }
+    return f;
+  }
+};
+
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
+// arguments, mask
+// ---------------------------------------------------------------------------
+template <typename T>
+struct SwaArgs {
+  const T* q;
+  const T* k;
+  const T* v;
+  const T* o;
+  const T* dout;
+  ssm_strides qs, ks, vs;
+  const int32_t* lens;
+  T* out;
+  float* lse;
+  T* dq;
+  T* dk;
+  T* dv;
+  float* delta;  // (Bs, Hq, Lq): sum of dout o
+  float* part;   // sinks: partial dk and dv
+  int Lq, Lk, Hq, Hk, G, W, S;
+  int nblk;      // blocks of queries (or keys) of a head
+  int nwork;     // workgroups
+  int nchunk;    // sinks: workgroups that share a block of keys
+  float scale;
+};
+
+// Query i stands at position p = i + Lk - Lq; it sees key j of [0, nk), nk the
+// row's key count, when j <= p and (p - j < W or j < S).
+struct Mask {
+  int nk, W, S;
+  __device__ __forceinline__ bool sees(int p, int j) const { return j <= p && j < nk && (p - j < W || j < S); }
+  // every position of [p0, p1] sees every key of [j0, j1]
+  __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
+    return j1 <= p0 && j1 < nk && (p1 - j0 < W || j1 < S);
+  }
+  // no position of [p0, p1] sees any key of [j0, j1]
+  __device__ __forceinline__ bool none(int p0, int p1, int j0, int j1) const {
+    return j0 > p1 || j0 >= nk || (p0 - j1 >= W && j0 >= S);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ Mask mask_of(const SwaArgs<T>& p, int b) {
+  int nk = p.Lk;
+  if (p.lens) {
+    nk = p.lens[b];
+    nk = nk < 0 ? 0 : nk > p.Lk ? p.Lk : nk;
+  }
+  return Mask{nk, p.W, p.S};
+}
+
+// Consecutive workgroups go to the eight XCDs in turn; consecutive work (the
+// heads that share keys, neighbouring blocks of a head) should share an L2.
+// The map deals each XCD a contiguous range.
+__device__ __forceinline__ int xcd_order(int blk, int n) {
+  const int per = n >> 3, rest = n & 7, x = blk & 7, i = blk >> 3;
+  // XCD x gets blocks x, x + 8, ...: per of them, one more if x < rest
+  return x * per + (x < rest ? x : rest) + i;
+}
+
+// The key tiles (of KB keys) that positions [p0, p1] may see: those of the
+// sinks before the window, then those of the window.
+struct KeyTiles {
+  int nsink, first, n;
+  __device__ __forceinline__ KeyTiles(const Mask& m, int p0, int p1, int KB) {
+    const int top = p1 < m.nk - 1 ? p1 : m.nk - 1;  // the last key seen
+    const int lo = p0 - m.W + 1 > 0 ? p0 - m.W + 1 : 0;
+    const int stop = top < m.S - 1 ? top : m.S - 1;
+    nsink = stop < 0 ? 0 : stop / KB + 1;
+    n = nsink;
+    first = 0;
+    if (top >= lo) {
+      first = lo / KB;
+      if (nsink > first) nsink = first;
+      n = nsink + top / KB - first + 1;
+    }
+  }
+  __device__ __forceinline__ int key0(int i, int KB) const { return (i < nsink ? i : first + i - nsink) * KB; }
+};
+
+__device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) <= 3.402823466e38f; }
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+template <typename T>
+bool swa_fits(int64_t v) { return v >= 0 && v <= (1 << 30); }
+
+}  // namespace
+
+#endif  // SSM_SWA_COMMON_H

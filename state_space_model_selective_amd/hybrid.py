@@ -29,6 +29,11 @@ PROTOTYPES = {
     "ssm_qk_rope_bwd_workspace_bytes": (_sz, [_i64] * 5 + [_ci]),
     "ssm_qk_rope_bwd": (_ci, [_vp] * 8 + [_f64] + [_vp] * 6 + [_i64] * 6 + [_ci, _vp, _sz, _vp]),
     "ssm_qk_rope_append": (_ci, [_vp] * 10 + [_f64] + [_vp] * 3 + [_i64] * 8 + [_ci, _vp]),
+    "ssm_swa_fwd": (_ci, [_vp] * 7 + [_f64] + [_vp] * 2 + [_i64] * 8 + [_ci, _vp]),
+    "ssm_swa_bwd_workspace_bytes": (_sz, [_i64] * 7 + [_ci]),
+    "ssm_swa_bwd": (_ci, [_vp] * 7 + [_f64] + [_vp] * 6 + [_i64] * 8 + [_ci, _vp, _sz, _vp]),
+    "ssm_swa_decode_workspace_bytes": (_sz, [_i64] * 5 + [_ci]),
+    "ssm_swa_decode": (_ci, [_vp] * 5 + [_f64, _vp] + [_i64] * 5 + [_ci, _vp, _sz, _vp]),
 }
 
 
@@ -368,3 +373,127 @@ def ssm_qk_rope_append(q, k, v, wq, wk, freq, pos, k_cache, v_cache, sinks, eps=
     _done(_pkg().lib().ssm_qk_rope_append(pq, sq, pk, sk, pv, sv, *rest, pp, eps, pqo, pkc, pvc, Bs, L, Hq, Hk, D, R,
                                           C - sinks, sinks, code, _raw_stream(dev, stream)), where)
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# attention with a sliding window and sinks
+# ---------------------------------------------------------------------------
+def _swa_args(where, q, k, v, window, sinks, scale, lens):
+    """What forward and backward share: (dims, dtype code, addresses up to lens, scale)."""
+    import torch
+    code = _lead(where, "q", q, 4)
+    dt, dev = q.dtype, q.device
+    Bs, Lq, Hq, D = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("%s: k must be a 4-D tensor (Bs, Lk, Hk, D)" % where)
+    Lk, Hk = k.shape[1], k.shape[2]
+    pq, sq = _strided(where, "q", q, dt, (Bs, Lq, Hq, D), dev)
+    pk, sk = _strided(where, "k", k, dt, (Bs, Lk, Hk, D), dev)
+    pv, sv = _strided(where, "v", v, dt, (Bs, Lk, Hk, D), dev)
+    if Hk < 1 or Hq < 1 or Hq % Hk:
+        raise ValueError("%s: the %d heads of q must be a multiple of the %d of k" % (where, Hq, Hk))
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError("%s: window must be at least 1 and sinks at least 0, got %d and %d" % (where, window, sinks))
+    pl = _maybe(where, "lens", lens, torch.int32, (Bs,), dev)
+    scale = D ** -0.5 if scale is None else float(scale)
+    return (Bs, Lq, Lk, Hq, Hk, D, window, sinks), code, (pq, sq, pk, sk, pv, sv, pl, scale)
+
+
+def ssm_swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=None, stream=None):
+    """Attention in which position p sees the keys j <= p with p - j < window
+    or j < sinks (and j < lens[b] if lens (Bs,) int32 is given). q (Bs, Lq,
+    Hq, D) stands at the last Lq of the Lk positions of k and v (Bs, Lk, Hk,
+    D); Hq is a multiple of Hk. They may be slices of a packed projection
+    (last dimension contiguous). scale is 1 / sqrt(D) if None. A query that
+    sees nothing gives zeros. Returns o (Bs, Lq, Hq, D), dense; with lse (Bs,
+    Hq, Lq) float32 the log of the softmax's sum is written there, for
+    ssm_swa_bwd."""
+    import torch
+    where = "ssm_swa_fwd"
+    dims, code, head = _swa_args(where, q, k, v, window, sinks, scale, lens)
+    Bs, Lq, _, Hq = dims[:4]
+    dev = q.device
+    po = _maybe(where, "o", o, q.dtype, q.shape, dev)
+    pl = _maybe(where, "lse", lse, torch.float32, (Bs, Hq, Lq), dev)
+    _gpu(where, q)
+    if o is None:
+        with _allocating(dev, stream):
+            o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        po = o.data_ptr()
+    _done(_pkg().lib().ssm_swa_fwd(*head, po, pl, *dims, code, _raw_stream(dev, stream)), where)
+    return o
+
+
+def ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, sinks=0, dtype=0):
+    return int(_pkg().lib().ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, sinks, int(dtype)))
+
+
+def ssm_swa_bwd(q, k, v, o, lse, do, window, sinks=0, scale=None, lens=None, out=None, workspace=None, stream=None):
+    """Gradients of sum(do * o) for o, lse of ssm_swa_fwd on the same
+    arguments: a dict with dq (like q), dk and dv (like k), dense. o and do
+    are dense. Tensors given in ``out`` (same keys) are written instead of new
+    ones."""
+    import torch
+    where = "ssm_swa_bwd"
+    dims, code, head = _swa_args(where, q, k, v, window, sinks, scale, lens)
+    Bs, Lq, Lk, Hq, Hk, D = dims[:6]
+    dt, dev = q.dtype, q.device
+    kinds = {"dq": (dt, q.shape), "dk": (dt, k.shape), "dv": (dt, k.shape)}
+    g = dict(out or {})
+    for n, t in g.items():
+        if n not in kinds:
+            raise ValueError("%s: unknown output %r" % (where, n))
+        _dense(where, n, t, *kinds[n], dev)
+    po, pdo = _dense(where, "o", o, dt, q.shape, dev), _dense(where, "do", do, dt, q.shape, dev)
+    pl = _dense(where, "lse", lse, torch.float32, (Bs, Hq, Lq), dev)
+    _gpu(where, q)
+    L_ = _pkg().lib()
+    with _allocating(dev, stream):
+        for n in kinds:
+            if n not in g:
+                g[n] = torch.empty(kinds[n][1], dtype=dt, device=dev)
+        ws, pw, nw = _workspace(where, workspace, L_.ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, dims[7], code), dev)
+    _done(L_.ssm_swa_bwd(*head, po, pl, pdo, g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), *dims, code,
+                         pw, nw, _raw_stream(dev, stream)), where)
+    return g
+
+
+def ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, dtype=0):
+    return int(_pkg().lib().ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, int(dtype)))
+
+
+def ssm_swa_decode(q, k_cache, v_cache, pos, scale=None, o=None, workspace=None, stream=None):
+    """One token of every row over the window cache that ssm_qk_rope_append
+    keeps: q (Bs, Hq, D) (last dimension contiguous) sees the min(pos + 1, C)
+    filled slots of k_cache and v_cache (Bs, Hk, C, D); pos (Bs,) int32 is the
+    token's position (negative: an inactive row, zeros). Returns o (Bs, Hq, D)."""
+    import torch
+    where = "ssm_swa_decode"
+    code = _lead(where, "q", q, 3)
+    dt, dev = q.dtype, q.device
+    Bs, Hq, D = q.shape
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("%s: k_cache must be a 4-D tensor (Bs, Hk, C, D)" % where)
+    Hk, C = k_cache.shape[1], k_cache.shape[2]
+    sq = None
+    if not q.is_contiguous():
+        if q.stride(2) != 1:
+            raise ValueError("%s: the last dimension of q must be contiguous" % where)
+        sq = ctypes.byref(SSMStrides(q.stride(0), 0, q.stride(1)))
+    pk = _dense(where, "k_cache", k_cache, dt, (Bs, Hk, C, D), dev)
+    pv = _dense(where, "v_cache", v_cache, dt, (Bs, Hk, C, D), dev)
+    if Hk < 1 or Hq < 1 or Hq % Hk:
+        raise ValueError("%s: the %d heads of q must be a multiple of the %d of k_cache" % (where, Hq, Hk))
+    pp = _dense(where, "pos", pos, torch.int32, (Bs,), dev)
+    po = _maybe(where, "o", o, dt, q.shape, dev)
+    _gpu(where, q)
+    L_ = _pkg().lib()
+    with _allocating(dev, stream):
+        if o is None:
+            o = torch.empty(q.shape, dtype=dt, device=dev)
+            po = o.data_ptr()
+        ws, pw, nw = _workspace(where, workspace, L_.ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, code), dev)
+    _done(L_.ssm_swa_decode(q.data_ptr(), sq, pk, pv, pp, D ** -0.5 if scale is None else float(scale), po, Bs, C, Hq,
+                            Hk, D, code, pw, nw, _raw_stream(dev, stream)), where)
+    return o

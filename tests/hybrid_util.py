@@ -167,3 +167,85 @@ def rope_reference(x, w, pos, freq, eps, d=None):
     dw, terms = (dn * u).sum((0, 1, 2)), x[..., 0].numel()
     e_dw = (e_dn * u.abs() + 11 * EPS * (dn * u).abs()).sum((0, 1, 2)) + EPS * min(terms, 1000) * (dn * u).abs().sum((0, 1, 2))
     return (value, err), (dx, e_dx), (dw, e_dw)
+
+
+# ---------------------------------------------------------------------------
+# attention with a sliding window and sinks
+# ---------------------------------------------------------------------------
+def swa_inputs(Bs, Lq, Lk, Hq, Hk, D, dtype, seed, lens=None):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g).to(dtype)
+    return dict(q=r(Bs, Lq, Hq, D), k=r(Bs, Lk, Hk, D), v=r(Bs, Lk, Hk, D), do=r(Bs, Lq, Hq, D),
+                lens=None if lens is None else torch.tensor(lens, dtype=torch.int32))
+
+
+def swa_seen(Lq, Lk, window, sinks, length):
+    p = torch.arange(Lq).unsqueeze(1) + (Lk - Lq)
+    j = torch.arange(Lk).unsqueeze(0)
+    return (j <= p) & (j < length) & ((p - j < window) | (j < sinks))
+
+
+def swa_reference(q, k, v, window, sinks, lens=None, do=None, scale=None, rounded_o=None):
+    """{name: (value, error before the store)} of o, lse and, with do, dq, dk, dv.
+
+    A score sums D products in float32 (D / 16 steps of an instruction, whose
+    own sum counts as one a term: D EPS of the sum of sizes), is multiplied by
+    scale log2 e (2) and has the reference point taken off (1). A weight has
+    that times ln 2 .. 1 (an absolute error of its exponent), the exponential
+    (2), and bfloat16 rounds it by half a step on its way into the product; the
+    sums over keys round once a tile at most, counted as Lk of them. delta
+    uses the stored o, as the kernel does; lse is stored in float32."""
+    dtype = q.dtype
+    half = half_step(dtype) if dtype == torch.bfloat16 else 0.0
+    Bs, Lq, Hq, D = q.shape
+    Lk, Hk = k.shape[1:3]
+    G = Hq // Hk
+    scale = D ** -0.5 if scale is None else scale
+    q, k, v = q.double(), k.double(), v.double()
+    z = lambda t: torch.zeros(t.shape, dtype=torch.float64)
+    o, eo = z(q), z(q)
+    lse, e_lse = (torch.zeros(Bs, Hq, Lq, dtype=torch.float64) for _ in range(2))
+    out = {"o": (o, eo), "lse": (lse, e_lse)}
+    if do is not None:
+        do = do.double()
+        out.update(dq=(z(q), z(q)), dk=(z(k), z(k)), dv=(z(v), z(v)))
+    for b in range(Bs):
+        seen = swa_seen(Lq, Lk, window, sinks, Lk if lens is None else int(lens[b]))
+        for h in range(Hq):
+            Q, K, V = q[b, :, h], k[b, :, h // G], v[b, :, h // G]
+            # unseen keys and values are left out, whatever they hold
+            K, V = (torch.where(seen.any(0).unsqueeze(1), t, torch.zeros_like(t)) for t in (K, V))
+            s = (Q @ K.T * scale).masked_fill(~seen, -math.inf)
+            es = scale * (D + 4) * EPS * (Q.abs() @ K.abs().T) + 4 * EPS * s.masked_fill(~seen, 0).abs()
+            L = torch.logsumexp(s, -1)
+            some = torch.isfinite(L)
+            P = torch.exp(s - torch.where(some, L, torch.zeros_like(L)).unsqueeze(1))
+            top = es.masked_fill(~seen, 0).amax(-1, keepdim=True) + 8 * EPS
+            ep = P * (es.masked_fill(~seen, 0) + top + 4 * EPS)        # of the unrounded, normalised weight
+            sums = (Lk + 8) * EPS
+            o[b, :, h] = P @ V
+            eo[b, :, h] = (ep + P * (half + sums)) @ V.abs()
+            lse[b, h] = L
+            e_lse[b, h] = top[:, 0] + sums + 4 * EPS * torch.where(some, L.abs(), torch.zeros_like(L))
+            if do is None:
+                continue
+            dO = do[b, :, h]
+            stored = o[b, :, h] if rounded_o is None else rounded_o[b, :, h].double()
+            delta = (dO * stored).sum(-1, keepdim=True)
+            # (the stored o is the kernel's own, so its error is in delta already; the sum adds D roundings)
+            e_delta = D * EPS * (dO * stored).abs().sum(-1, keepdim=True)
+            dP = dO @ V.T
+            e_dP = (D + 2) * EPS * (dO.abs() @ V.abs().T)
+            # lse is stored: another rounding of it reaches the weight
+            ep = ep + P * (e_lse[b, h] + EPS * torch.where(some, L.abs(), torch.zeros_like(L))).unsqueeze(1)
+            exact_delta = (dO * o[b, :, h]).sum(-1, keepdim=True)
+            dS = P * (dP - exact_delta)
+            e_ds = ep * (dP - delta).abs() + P * (e_dP + e_delta + (delta - exact_delta).abs()) + 2 * EPS * dS.abs()
+            out["dq"][0][b, :, h] = scale * dS @ K
+            out["dq"][1][b, :, h] = scale * (e_ds + dS.abs() * (half + sums) + e_ds * half) @ K.abs()
+            many = (Lq * G + 8) * EPS
+            out["dk"][0][b, :, h // G] += scale * dS.T @ Q
+            out["dk"][1][b, :, h // G] += scale * (e_ds + dS.abs() * (half + many) + e_ds * half).T @ Q.abs()
+            out["dv"][0][b, :, h // G] += P.T @ dO
+            out["dv"][1][b, :, h // G] += (ep + P * (half + many) + ep * half).T @ dO.abs()
+    return out

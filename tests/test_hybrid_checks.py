@@ -9,7 +9,7 @@ import torch
 
 import state_space_model_selective_amd as ssm
 from state_space_model_selective_amd import hybrid
-from hybrid_util import glr_inputs, glr_reference, rope_inputs, rope_reference
+from hybrid_util import glr_inputs, glr_reference, rope_inputs, rope_reference, swa_inputs, swa_reference, swa_seen
 
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ssm_hybrid.h")
 f32, bf16 = torch.float32, torch.bfloat16
@@ -224,8 +224,9 @@ def test_rope_abi_refusals(fn):
     call = lambda **kw: c_rope(fn, **kw)
     for n in ("q", "k", "freq", "qo", "ko"):
         assert call(**{n: None}) == ssm.SSM_ERR_NULL, n
-    for n in ("q", "wq", "pos", "freq", "ko"):
+    for n in ("q", "wq", "freq", "ko"):
         assert call(**{n: P[20] + 8}) == ssm.SSM_ERR_UNSUPPORTED, n
+    assert call(pos=P[20] + 2) == ssm.SSM_ERR_UNSUPPORTED
     for n in ("Bs", "L", "Hq", "Hk"):
         assert call(**{n: -1}) == ssm.SSM_ERR_DIM, n
     assert call(Bs=1 << 40, L=1 << 20) == ssm.SSM_ERR_DIM
@@ -265,3 +266,114 @@ def test_rope_reference_gradient():
     dq, dw = torch.autograd.grad(loss, (q, w))
     _, dx, dwr = rope_reference(t["q"], t["wq"], t["pos"], t["freq"], 1e-6, t["dq_out"])
     assert torch.allclose(dx[0], dq, rtol=1e-9, atol=1e-12) and torch.allclose(dwr[0], dw, rtol=1e-9, atol=1e-12)
+
+
+# --- attention ---------------------------------------------------------------
+def swa(dtype=f32):
+    t = swa_inputs(2, 6, 9, 4, 2, 64, dtype, seed=0)
+    return {n: t[n] for n in "qkv"}, t
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_swa_valid_arguments_reach_the_gpu_check(dtype):
+    a, t = swa(dtype)
+    lse, lens = torch.zeros(2, 4, 6), torch.zeros(2, dtype=torch.int32)
+    gpu_only(ssm.ssm_swa_fwd, **a, window=4, sinks=1, lens=lens, lse=lse, o=torch.empty_like(t["q"]))
+    gpu_only(ssm.ssm_swa_bwd, **a, o=t["q"], lse=lse, do=t["do"], window=4, out={"dk": torch.empty_like(t["k"])})
+    gpu_only(ssm.ssm_swa_decode, t["q"][:, 0], torch.zeros(2, 2, 9, 64, dtype=dtype), torch.zeros(2, 2, 9, 64, dtype=dtype), lens)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("q", torch.zeros(2, 6, 256)), ("q", torch.zeros(2, 6, 4, 64, dtype=torch.float64)), ("k", torch.zeros(2, 9, 2, 32)),
+    ("k", torch.zeros(2, 9, 64)), ("v", torch.zeros(2, 8, 2, 64)), ("v", torch.zeros(2, 9, 2, 64, dtype=bf16)),
+    ("v", torch.zeros(2, 9, 64, 2).transpose(2, 3)), ("k", torch.zeros(3, 9, 2, 64)), ("window", 0), ("sinks", -1),
+    ("lens", torch.zeros(2)), ("lens", torch.zeros(3, dtype=torch.int32)), ("lse", torch.zeros(2, 6, 4)),
+    ("o", torch.zeros(2, 6, 4, 64, dtype=bf16)), ("v", None), ("lens", torch.zeros(2, dtype=torch.int32, device="meta"))])
+def test_swa_refusals(name, bad):
+    a, _ = swa()
+    refuses(name, ssm.ssm_swa_fwd, **dict(dict(a, window=4), **{name: bad}))
+
+
+def test_swa_heads_refused():
+    a, t = swa()
+    refuses("multiple", ssm.ssm_swa_fwd, t["q"][:, :, :3], t["k"], t["v"], 4)
+    c = torch.zeros(2, 3, 9, 64)
+    pos = torch.zeros(2, dtype=torch.int32)
+    refuses("multiple", ssm.ssm_swa_decode, t["q"][:, 0], c, c, pos)
+    d = torch.zeros(2, 2, 9, 64)
+    refuses("pos", ssm.ssm_swa_decode, t["q"][:, 0], d, d, pos.long())
+    refuses("v_cache", ssm.ssm_swa_decode, t["q"][:, 0], d, d[:, :, :8], pos)
+    refuses("k_cache", ssm.ssm_swa_decode, t["q"][:, 0], d.transpose(1, 2), d, pos)
+    lse = torch.zeros(2, 4, 6)
+    refuses("lse", ssm.ssm_swa_bwd, **a, o=t["q"], lse=None, do=t["do"], window=4)
+    refuses("do", ssm.ssm_swa_bwd, **a, o=t["q"], lse=lse, do=t["do"][:, :5], window=4)
+    refuses("unknown output", ssm.ssm_swa_bwd, **a, o=t["q"], lse=lse, do=t["do"], window=4, out={"dx": lse})
+
+
+def c_swa(fn, **kw):
+    v = dict(q=P[0], qs=None, k=P[1], ks=None, v=P[2], vs=None, lens=P[3], scale=0.125, o=P[4], lse=P[5], do=P[6], dq=P[7],
+             dk=P[8], dv=P[9], pos=P[3], Bs=2, Lq=8, Lk=8, C=2000, Hq=4, Hk=2, D=64, window=16, sinks=4, dt=0, ws=P[13], wb=1 << 30)
+    v.update(kw)
+    names = {"ssm_swa_fwd": "q qs k ks v vs lens scale o lse Bs Lq Lk Hq Hk D window sinks dt",
+             "ssm_swa_bwd": "q qs k ks v vs lens scale o lse do dq dk dv Bs Lq Lk Hq Hk D window sinks dt ws wb",
+             "ssm_swa_decode": "q qs k v pos scale o Bs C Hq Hk D dt ws wb"}[fn]
+    args = [ctypes.byref(v[n]) if isinstance(v[n], ctypes.Structure) else v[n] for n in names.split()]
+    return getattr(ssm.lib(), fn)(*args, None)
+
+
+@host_only
+@pytest.mark.parametrize("fn", ["ssm_swa_fwd", "ssm_swa_bwd", "ssm_swa_decode"])
+def test_swa_abi_refusals(fn):
+    call = lambda **kw: c_swa(fn, **kw)
+    for n in ("q", "k", "v", "o"):
+        assert call(**{n: None}) == ssm.SSM_ERR_NULL, n
+    for n in ("q", "k", "v", "o"):
+        assert call(**{n: P[20] + 8}) == ssm.SSM_ERR_UNSUPPORTED, n
+    for kw in (dict(Bs=-1), dict(Hq=3), dict(Hk=0), dict(Hq=0), dict(Bs=1 << 50)):
+        assert call(**kw) == ssm.SSM_ERR_DIM, kw
+    for kw in (dict(D=32), dict(D=96), dict(dt=2)):
+        assert call(**kw) == ssm.SSM_ERR_UNSUPPORTED, kw
+    for bad in (0.0, -1.0, float("nan"), float("inf")):
+        assert call(scale=bad) == ssm.SSM_ERR_ARG
+    S = hybrid.SSMStrides
+    assert call(qs=S(512, 256, 66)) == ssm.SSM_ERR_UNSUPPORTED
+    assert call(qs=S(-512, 256, 64)) == ssm.SSM_ERR_UNSUPPORTED
+    if fn != "ssm_swa_bwd":
+        assert call(o=P[0]) == ssm.SSM_ERR_ALIAS and call(o=P[2]) == ssm.SSM_ERR_ALIAS
+    none = dict(q=None, k=None, v=None, o=None, lse=None, do=None, dq=None, dk=None, dv=None, pos=None, lens=None)
+    assert call(**dict(none, Bs=0)) == ssm.SSM_OK
+
+
+@host_only
+def test_swa_abi_refusals_of_one():
+    for fn in ("ssm_swa_fwd", "ssm_swa_bwd"):
+        for kw in (dict(Lq=-1), dict(Lk=(1 << 30) + 1), dict(window=0), dict(sinks=-1)):
+            assert c_swa(fn, **kw) == ssm.SSM_ERR_DIM, kw
+        assert c_swa(fn, ks=hybrid.SSMStrides(512, 1 << 24, 64)) == ssm.SSM_ERR_UNSUPPORTED  # token stride past 32 MiB
+    assert c_swa("ssm_swa_fwd", lse=P[4]) == ssm.SSM_ERR_ALIAS
+    for n in ("lse", "do", "dq", "dk", "dv"):
+        assert c_swa("ssm_swa_bwd", **{n: None}) == ssm.SSM_ERR_NULL, n
+    assert c_swa("ssm_swa_bwd", dk=P[7]) == ssm.SSM_ERR_ALIAS
+    assert c_swa("ssm_swa_bwd", ws=None) == ssm.SSM_ERR_WORKSPACE
+    assert c_swa("ssm_swa_bwd", wb=16) == ssm.SSM_ERR_WORKSPACE
+    assert c_swa("ssm_swa_decode", pos=None) == ssm.SSM_ERR_NULL
+    assert c_swa("ssm_swa_decode", C=-1) == ssm.SSM_ERR_DIM
+    assert ssm.ssm_swa_decode_workspace_bytes(2, 2000, 4, 2, 64) > 0
+    assert c_swa("ssm_swa_decode", ws=None) == ssm.SSM_ERR_WORKSPACE
+    assert c_swa("ssm_swa_decode", ws=P[1]) == ssm.SSM_ERR_ALIAS
+
+
+def test_swa_reference_gradient():
+    t = swa_inputs(2, 7, 10, 4, 2, 64, f32, seed=1, lens=[10, 5])
+    leaves = [t[n].double().requires_grad_() for n in "qkv"]
+    q, k, v = leaves
+    loss = 0
+    for b in range(2):
+        seen = swa_seen(7, 10, 3, 1, int(t["lens"][b]))
+        for h in range(4):
+            s = (q[b, :, h] @ k[b, :, h // 2].T / 8).masked_fill(~seen, -1e300)
+            p = torch.where(seen.any(1, keepdim=True), torch.softmax(s, -1), torch.zeros_like(s))
+            loss = loss + ((p @ v[b, :, h // 2]) * t["do"][b, :, h].double()).sum()
+    ref = swa_reference(**t, window=3, sinks=1)
+    for n, g in zip("qkv", torch.autograd.grad(loss, leaves)):
+        assert torch.allclose(ref["d" + n][0], g, rtol=1e-9, atol=1e-11), n

@@ -1,0 +1,290 @@
+"""Attention with a sliding window and sinks on the GPU against its 64-bit definition."""
+import math
+
+import pytest
+import torch
+
+import state_space_model_selective_amd as ssm
+from hybrid_util import half_step, rounded, swa_inputs, swa_reference, swa_seen, within
+from parity_util import log
+from test_graph_gpu import replay_check
+
+pytestmark = pytest.mark.gpu
+
+f32, bf16 = torch.float32, torch.bfloat16
+
+# (Bs, Lq, Lk, Hq, Hk, D, window, sinks, lens): single tokens, lengths around the tiles, windows of one key and wider
+# than the sequence, sinks inside and past the window, more and fewer queries than keys, empty and full padded rows
+CASES = [
+    (1, 1, 1, 1, 1, 64, 1, 0, None),
+    (2, 5, 5, 2, 1, 64, 2, 1, None),
+    (1, 33, 33, 4, 2, 128, 8, 0, None),
+    (1, 64, 64, 2, 2, 64, 64, 0, None),
+    (2, 65, 65, 3, 1, 128, 1000, 3, None),
+    (1, 130, 130, 2, 1, 64, 1, 5, None),
+    (1, 129, 300, 2, 1, 128, 50, 4, None),
+    (2, 200, 90, 2, 1, 64, 33, 2, None),
+    (1, 1, 700, 6, 2, 128, 200, 70, None),
+    (3, 150, 150, 4, 4, 64, 40, 6, [0, 150, 37]),
+    (2, 257, 257, 6, 2, 64, 100, 130, [257, 1]),
+    (1, 520, 520, 8, 1, 128, 128, 4, None),
+    (1, 300, 300, 1, 1, 64, 7, 400, None),
+    (4, 70, 70, 5, 5, 128, 16, 0, [70, 64, 3, 0]),
+]
+
+
+def cuda(t):
+    return {k: None if v is None else v.cuda() for k, v in t.items()}
+
+
+def train(g, window, sinks, **kw):
+    q = g["q"]
+    lse = torch.full((q.shape[0], q.shape[2], q.shape[1]), float("nan"), device="cuda")
+    o = ssm.ssm_swa_fwd(q, g["k"], g["v"], window, sinks, lens=g["lens"], lse=lse, **kw)
+    grads = ssm.ssm_swa_bwd(q, g["k"], g["v"], o, lse, g["do"], window, sinks, lens=g["lens"], **kw)
+    return {"o": o, "lse": lse, **grads}
+
+
+def check(t, out, window, sinks, **kw):
+    ref = swa_reference(**t, window=window, sinks=sinks, rounded_o=out["o"].cpu(), **kw)
+    for n, got in out.items():
+        value, err = ref[n]
+        if n == "lse":
+            none = torch.isinf(value)
+            assert torch.equal(torch.isinf(got.cpu()), none) and bool((got.cpu()[none] < 0).all())
+            got, value, err = got.cpu()[~none], value[~none], err[~none]
+        within(n, got, value, rounded(value, err, got.dtype))
+    return ref
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("case", CASES)
+def test_forward_and_gradients(case, dtype):
+    log("swa %s %s" % (case, dtype))
+    Bs, Lq, Lk, Hq, Hk, D, window, sinks, lens = case
+    t = swa_inputs(Bs, Lq, Lk, Hq, Hk, D, dtype, seed=Lq + Lk, lens=lens)
+    check(t, train(cuda(t), window, sinks), window, sinks)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_rows_that_see_nothing_are_zero(dtype):
+    t = swa_inputs(3, 40, 30, 2, 1, 64, dtype, seed=1, lens=[0, 30, 4])
+    out = train(cuda(t), 8, 0)
+    for b, n in enumerate([0, 30, 4]):
+        none = ~swa_seen(40, 30, 8, 0, n).any(1)
+        assert bool(none.any())
+        assert float(out["o"][b, none.cuda()].abs().max()) == 0 and float(out["dq"][b, none.cuda()].abs().max()) == 0
+        assert bool((out["lse"][b][:, none.cuda()] == -math.inf).all())
+    assert float(out["dk"][0].abs().max()) == 0 and float(out["dv"][0].abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_slices_of_a_packed_projection(dtype):
+    """q, k and v in place in one tensor, and head-major in memory: the same bits as dense tensors."""
+    Bs, L, Hq, Hk, D = 2, 150, 6, 2, 64
+    t = swa_inputs(Bs, L, L, Hq, Hk, D, dtype, seed=2)
+    g = cuda(t)
+    want = train(g, 40, 3)
+    packed = torch.cat([g["q"], g["k"], g["v"]], 2)
+    part = dict(g, q=packed[:, :, :Hq], k=packed[:, :, Hq:Hq + Hk], v=packed[:, :, Hq + Hk:])
+    major = dict(g, **{n: g[n].transpose(1, 2).contiguous().transpose(1, 2) for n in "qkv"})
+    for other in (part, major):
+        for n, v in train(other, 40, 3).items():
+            assert torch.equal(v, want[n]), n
+
+
+def test_repeated_key_head():
+    """One key head under every query head, by a stride of zero or as Hk = 1: the same output."""
+    t = cuda(swa_inputs(1, 100, 100, 4, 1, 64, bf16, seed=3))
+    one = ssm.ssm_swa_fwd(t["q"], t["k"], t["v"], 30, 2)
+    many = ssm.ssm_swa_fwd(t["q"], t["k"].expand(1, 100, 4, 64), t["v"].expand(1, 100, 4, 64), 30, 2)
+    assert torch.equal(one, many)
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_unseen_values_that_are_not_finite(bad, dtype):
+    """What padded rows, later keys and keys before the window hold does not reach the queries that do not see them."""
+    Bs, L, window, sinks = 2, 200, 30, 2
+    t = swa_inputs(Bs, L, L, 2, 1, 64, dtype, seed=4, lens=[120, 200])
+    want = train(cuda(t), window, sinks)
+    t["k"][0, 120:], t["v"][0, 120:] = bad, bad       # padding: seen by nobody
+    t["v"][1, 100] = bad                              # seen by queries 100 .. 129 alone
+    out = train(cuda(t), window, sinks)
+    hit = torch.zeros(L, dtype=torch.bool)
+    hit[100:130] = True
+    for n in ("o", "dq"):
+        assert torch.equal(out[n][0], want[n][0]), n
+        assert torch.allclose(out[n][1][~hit.cuda()].float(), want[n][1][~hit.cuda()].float(), rtol=2 ** -6, atol=2e-2), n
+        assert not bool(torch.isfinite(out[n][1][hit.cuda()]).all(-1).any()), n
+    # dk and dv of the keys that no hit query sees
+    touched = swa_seen(L, L, window, sinks, L)[hit].any(0)
+    for n in ("dk", "dv"):
+        assert torch.equal(out[n][0], want[n][0]), n
+        keep = (~touched).cuda()
+        assert torch.allclose(out[n][1][keep].float(), want[n][1][keep].float(), rtol=2 ** -6, atol=2e-2), n
+
+
+def test_query_that_is_not_finite():
+    """A NaN query spoils its own row and the gradients of the keys that it sees, nothing else."""
+    L, window, sinks = 200, 30, 2
+    t = swa_inputs(1, L, L, 2, 1, 64, bf16, seed=5)
+    want = train(cuda(t), window, sinks)
+    t["q"][0, 90, 1] = float("nan")
+    out = train(cuda(t), window, sinks)
+    keep = torch.ones(L, 2, dtype=torch.bool)
+    keep[90, 1] = False
+    for n in ("o", "dq"):
+        assert torch.allclose(out[n][0][keep.cuda()].float(), want[n][0][keep.cuda()].float(), rtol=2 ** -6, atol=2e-2), n
+        assert bool(torch.isnan(out[n][0, 90, 1]).all())
+    touched = swa_seen(L, L, window, sinks, L)[90]
+    for n in ("dk", "dv"):
+        assert torch.allclose(out[n][0][~touched.cuda()].float(), want[n][0][~touched.cuda()].float(), rtol=2 ** -6, atol=2e-2), n
+        assert bool(torch.isnan(out[n][0][touched.cuda()]).all()), n
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_large_scores(dtype):
+    """Scores of some hundreds: the weights of all but a few keys vanish, nothing overflows. The float32 score's own
+    error grows with its size, as the bound says."""
+    t = swa_inputs(1, 150, 150, 2, 1, 64, dtype, seed=6)
+    t["q"] *= 20
+    check(t, train(cuda(t), 60, 2), 60, 2)
+
+
+def test_scale():
+    t = swa_inputs(1, 90, 90, 2, 1, 64, f32, seed=7)
+    check(t, train(cuda(t), 60, 2, scale=0.3), 60, 2, scale=0.3)
+
+
+def test_equal_keys_share_the_weight():
+    """All scores equal: the mean of the values seen."""
+    t = swa_inputs(1, 300, 300, 1, 1, 64, f32, seed=8)
+    t["k"][:] = 0
+    o = ssm.ssm_swa_fwd(*(t[n].cuda() for n in "qkv"), 100, 3).cpu().double()
+    seen = swa_seen(300, 300, 100, 3, 300).double()
+    mean = (seen / seen.sum(1, keepdim=True)) @ t["v"][0, :, 0].double()
+    assert float((o[0, :, 0] - mean).abs().max()) <= 110 * 2 ** -24 * float(t["v"].abs().max())
+
+
+# --- single tokens -----------------------------------------------------------
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("Bs,Hq,Hk,D,C", [(1, 1, 1, 64, 1), (6, 4, 2, 64, 33), (6, 8, 1, 128, 500), (6, 2, 2, 128, 2052),
+                                          (6, 40, 1, 64, 200), (6, 24, 8, 128, 128), (300, 4, 2, 64, 70)])
+def test_decode(Bs, Hq, Hk, D, C, dtype):
+    log("swa_decode %d x %d, %d x %d over %d %s" % (Bs, Hq, Hk, D, C, dtype))
+    g = torch.Generator().manual_seed(C)
+    q = torch.randn(Bs, Hq, D, generator=g).to(dtype)
+    kc, vc = (torch.randn(Bs, Hk, C, D, generator=g).to(dtype) for _ in range(2))
+    pos = torch.randint(-2, 2 * C, (Bs,), generator=g, dtype=torch.int32)
+    pos[:6] = torch.tensor([0, -1, C - 1, C, 10 ** 9, C // 2], dtype=torch.int32)[:Bs]
+    for b in range(Bs):  # what unfilled slots hold does not matter
+        n = max(0, min(int(pos[b]) + 1, C))
+        kc[b, :, n:], vc[b, :, n:] = float("nan"), float("inf")
+    got = ssm.ssm_swa_decode(q.cuda(), kc.cuda(), vc.cuda(), pos.cuda())
+    # the same query as the last of a sequence that the cache holds, seeing all of it
+    for b in range(min(Bs, 8)):
+        n = max(0, min(int(pos[b]) + 1, C))
+        if n == 0:
+            assert float(got[b].abs().max()) == 0
+            continue
+        ref = swa_reference(q[b].view(1, 1, Hq, D), kc[b:b + 1, :, :n].transpose(1, 2), vc[b:b + 1, :, :n].transpose(1, 2), n, 0)
+        value, err = ref["o"]
+        within("o[%d]" % b, got[b], value[0, 0], rounded(value, err, dtype)[0, 0])
+
+
+def test_decode_follows_the_forward():
+    """Tokens appended and decoded one by one give the rows of the forward over the whole sequence."""
+    Bs, L, Hq, Hk, D, window, sinks = 2, 90, 4, 2, 64, 20, 3
+    t = cuda(swa_inputs(Bs, L, L, Hq, Hk, D, f32, seed=9))
+    whole = ssm.ssm_swa_fwd(t["q"], t["k"], t["v"], window, sinks)
+    kc, vc = (torch.full((Bs, Hk, sinks + window, D), float("nan"), device="cuda") for _ in range(2))
+    for i in range(L):
+        pos = torch.full((Bs,), i, dtype=torch.int32, device="cuda")
+        slot = i if i < sinks else sinks + (i - sinks) % window
+        kc[:, :, slot], vc[:, :, slot] = t["k"][:, i], t["v"][:, i]
+        o = ssm.ssm_swa_decode(t["q"][:, i], kc, vc, pos)
+        # float32 on both sides: a few roundings a key apart
+        assert float((o - whole[:, i]).abs().max()) <= 64 * 2 ** -24 * float(t["v"].abs().max()), i
+
+
+# --- the rest ----------------------------------------------------------------
+def test_empty():
+    z = lambda *s: torch.zeros(*s, device="cuda")
+    assert ssm.ssm_swa_fwd(z(0, 4, 2, 64), z(0, 4, 1, 64), z(0, 4, 1, 64), 8).shape == (0, 4, 2, 64)
+    assert ssm.ssm_swa_fwd(z(2, 0, 2, 64), z(2, 4, 1, 64), z(2, 4, 1, 64), 8).shape == (2, 0, 2, 64)
+    lse = z(2, 2, 4)
+    q = torch.ones(2, 4, 2, 64, device="cuda")
+    o = ssm.ssm_swa_fwd(q, z(2, 0, 1, 64), z(2, 0, 1, 64), 8, 1, lse=lse)
+    assert float(o.abs().max()) == 0 and bool((lse == -math.inf).all())
+    g = ssm.ssm_swa_bwd(q, z(2, 0, 1, 64), z(2, 0, 1, 64), o, lse, q, 8, 1)
+    assert float(g["dq"].abs().max()) == 0 and g["dk"].shape == (2, 0, 1, 64)
+    g = ssm.ssm_swa_bwd(z(2, 0, 2, 64), q[:, :, :1].contiguous(), q[:, :, :1].contiguous(), z(2, 0, 2, 64), z(2, 2, 0), z(2, 0, 2, 64), 8)
+    assert float(g["dk"].abs().max()) == 0 and float(g["dv"].abs().max()) == 0
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert float(ssm.ssm_swa_decode(q[:, 0], z(2, 1, 0, 64), z(2, 1, 0, 64), i).abs().max()) == 0
+    assert ssm.ssm_swa_decode(z(0, 2, 64), z(0, 1, 4, 64), z(0, 1, 4, 64), i[:0]).shape == (0, 2, 64)
+
+
+def test_gradient_against_differences():
+    t = cuda(swa_inputs(1, 40, 40, 2, 1, 64, f32, seed=10))
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    v = {n: torch.randn(t[n].shape, generator=gen, device="cuda") for n in "qkv"}
+
+    def loss(step):
+        o = ssm.ssm_swa_fwd(*(t[n] + step * v[n] for n in "qkv"), 12, 2)
+        return float((o.double() * t["do"].double()).sum())
+
+    out = train(t, 12, 2)
+    want = sum(float((out["d" + n].double() * v[n].double()).sum()) for n in "qkv")
+    eps = 1e-2
+    got = (8 * (loss(eps) - loss(-eps)) - (loss(2 * eps) - loss(-2 * eps))) / (12 * eps)
+    size = sum(float((out["d" + n].double() * v[n].double()).square().sum()) for n in "qkv") ** 0.5
+    assert abs(got - want) <= 1e-3 * size, (got, want, size)
+
+
+def test_repeated_calls_streams_and_graph():
+    g = cuda(swa_inputs(2, 500, 500, 4, 2, 128, bf16, seed=11, lens=[500, 311]))
+    first = train(g, 150, 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = train(g, 150, 5)
+    with torch.cuda.stream(side):
+        aside = train(g, 150, 5)
+    side.synchronize()
+    for out in (other, aside):
+        for n, v in out.items():
+            assert torch.equal(v, first[n]), n
+    o, lse = torch.empty_like(first["o"]), torch.zeros_like(first["lse"])
+    grads = {n: torch.empty_like(first[n]) for n in ("dq", "dk", "dv")}
+
+    def both():
+        ssm.ssm_swa_fwd(g["q"], g["k"], g["v"], 150, 5, o=o, lse=lse)
+        ssm.ssm_swa_bwd(g["q"], g["k"], g["v"], o, lse, g["do"], 150, 5, out=grads)
+
+    replay_check("window attention", both, [o, lse] + list(grads.values()))
+    pos = torch.tensor([700, 30], dtype=torch.int32, device="cuda")
+    kc, vc = (g[n][:, :300].transpose(1, 2).contiguous() for n in "kv")
+    one = torch.empty(2, 4, 128, dtype=bf16, device="cuda")
+    replay_check("window attention, one token", lambda: ssm.ssm_swa_decode(g["q"][:, 0], kc, vc, pos, o=one), [one])
+
+
+def test_long_offsets():
+    """A batch row whose keys start past 2^31 elements."""
+    k = torch.empty(1 << 17, 132, 128, dtype=bf16, device="cuda")  # 2.2e9 elements
+    rows = k.view(1, -1, 132, 128)
+    t = cuda(swa_inputs(1, 64, 64, 4, 4, 128, bf16, seed=12))
+    rows[0, -64:, 128:] = t["k"][0]
+    got = ssm.ssm_swa_fwd(t["q"], rows[:, -64:, 128:], t["v"], 30, 2)
+    assert torch.equal(got, ssm.ssm_swa_fwd(t["q"], t["k"], t["v"], 30, 2))
+    # a cache whose last row starts past 2^31 elements
+    cache = torch.zeros(260, 1, 1 << 16, 128, dtype=bf16, device="cuda")
+    few = torch.randn(1, 1, 100, 128, device="cuda").to(bf16)
+    cache[-1, :, :100] = few
+    pos = torch.full((260,), -1, dtype=torch.int32, device="cuda")
+    pos[-1] = 99
+    q = torch.randn(260, 2, 128, device="cuda").to(bf16)
+    o = ssm.ssm_swa_decode(q, cache, cache, pos)
+    want = ssm.ssm_swa_decode(q[-1:], few, few, pos[-1:])
+    # (split among workgroups differently: the weights' roundings to bfloat16 differ)
+    assert torch.allclose(o[-1].float(), want[0].float(), rtol=2 ** -6, atol=2e-2) and float(o[:-1].abs().max()) == 0
