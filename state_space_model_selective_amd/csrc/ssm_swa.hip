@@ -21,11 +21,20 @@
 namespace {
 
 constexpr int kWaves = 4, kNT = 64 * kWaves;
-constexpr int kOwn = 32 * kWaves;  // queries (or keys) of a workgroup
 
-// rows of an LDS tile: 16 KiB of them, at most 64
-template <typename T, int D>
-constexpr int kRows = 16384 / (D * static_cast<int>(sizeof(T))) < 64 ? 32 : 64;
+// Two ways for the four waves of a workgroup to share its work. Apart: each
+// owns 32 rows (queries; keys for dk and dv) and they go over the same tiles,
+// double-buffered. Together (SPLIT): all own the same 32 rows, tiles are four
+// blocks of 32, a wave takes one, and the waves' sums are added at the end --
+// four times the workgroups, for calls that would leave compute units empty.
+template <typename T, int D, bool SPLIT>
+struct Shape {
+  static constexpr int kOwn = SPLIT ? 32 : 32 * kWaves;  // rows of a workgroup
+  // rows of an LDS tile; apart: 16 KiB of them, at most 64
+  static constexpr int kRows = SPLIT ? 32 * kWaves : 16384 / (D * static_cast<int>(sizeof(T))) < 64 ? 32 : 64;
+  static constexpr int kBufs = SPLIT ? 1 : 2;
+  static constexpr int kBlocks = SPLIT ? 1 : kRows / 32;  // blocks of a tile that a wave takes
+};
 
 template <typename T>
 struct Place {
@@ -190,22 +199,80 @@ __device__ __forceinline__ bool all_finite(const v16f (&x)[D / 32], float mul) {
   return s == 0.f;
 }
 
+// The sum over the four waves of a result tile set, left in wave 0: (x0 + x2)
+// + (x1 + x3), through LDS rows of D + 4 floats (16-byte accesses of lanes on
+// neighbouring rows then touch different banks). Everybody calls it.
+template <int D>
+__device__ __forceinline__ void add_waves(v16f (&x)[D / 32], char* lds, int wave, int n, int hi) {
+  constexpr int P = D + 4;
+  float* area = reinterpret_cast<float*>(lds) + (wave & 1) * 32 * P + n * P + 4 * hi;
+#pragma unroll
+  for (int step = 2; step >= 1; step >>= 1) {
+    __syncthreads();
+    if (wave >= step && wave < 2 * step)
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<float4*>(area + 32 * db + 8 * r) =
+              make_float4(x[db][4 * r], x[db][4 * r + 1], x[db][4 * r + 2], x[db][4 * r + 3]);
+    __syncthreads();
+    if (wave < step) {
+      // (at the last step wave 0 reads wave 1's rows)
+      const float* from = step == 2 ? area : area + 32 * P;
+#pragma unroll
+      for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 v = *reinterpret_cast<const float4*>(from + 32 * db + 8 * r);
+          x[db][4 * r] += v.x, x[db][4 * r + 1] += v.y, x[db][4 * r + 2] += v.z, x[db][4 * r + 3] += v.w;
+        }
+    }
+  }
+}
+
+// The tiles 0 .. n - 1 of a workgroup: load(t, buffer) starts the loads of a
+// tile, use(t, buffer) works on it. Apart, the next tile's loads are under way
+// while this one is used.
+template <bool SPLIT, typename L, typename U>
+__device__ __forceinline__ void over_tiles(int n, L load, U use) {
+  if constexpr (SPLIT) {
+    for (int t = 0; t < n; ++t) {
+      __syncthreads();  // nobody reads the last tile any more
+      load(t, 0);
+      wait_loads();
+      __syncthreads();
+      use(t, 0);
+    }
+  } else {
+    __syncthreads();
+    if (n > 0) load(0, 0);
+    for (int t = 0; t < n; ++t) {
+      wait_loads();
+      __syncthreads();  // tile t is in LDS; nobody reads the other buffer any more
+      if (t + 1 < n) load(t + 1, (t + 1) & 1);
+      use(t, t & 1);
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
-  constexpr int KB = kRows<T, D>, NB = KB / 32, KK = D / 16, DB = D / 32;
+  using Z = Shape<T, D, SPLIT>;
+  constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
-  __shared__ __attribute__((aligned(16))) char sm[2][2][KT::kBytes];
+  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][KT::kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, hi = lane >> 5;
   const Place<T> w = place_q(p);
   const Mask m = mask_of(p, w.b);
-  const int off = p.Lk - p.Lq, i0 = w.blk * kOwn + 32 * wave, i = i0 + n;
-  const int pos = i + off, pw0 = i0 + off, pw1 = pw0 + 31;
-  const int last_i = w.blk * kOwn + kOwn - 1 < p.Lq - 1 ? w.blk * kOwn + kOwn - 1 : p.Lq - 1;
-  const KeyTiles tiles(m, w.blk * kOwn + off, last_i + off, KB);
+  const int off = p.Lk - p.Lq, ib = w.blk * Z::kOwn, i0 = SPLIT ? ib : ib + 32 * wave, i = i0 + n;
+  const int pos = i + off, pw0 = i0 + off, pw1 = (i0 + 31 < p.Lq ? i0 + 31 : p.Lq - 1) + off;
+  const int last_i = ib + Z::kOwn < p.Lq ? ib + Z::kOwn - 1 : p.Lq - 1;
+  const KeyTiles tiles(m, ib + off, last_i + off, KB);
   const T* kbase = p.k + w.b * p.ks.batch + w.hk * p.ks.head;
   const T* vbase = p.v + w.b * p.vs.batch + w.hk * p.vs.head;
 
@@ -221,65 +288,79 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = v16f{};
 
-  if (tiles.n > 0) {
-    const int k0 = tiles.key0(0, KB);
-    KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[0][0], wave, lane);
-    KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[0][1], wave, lane);
-  }
-  for (int t = 0; t < tiles.n; ++t) {
-    wait_loads();
-    __syncthreads();  // tile t is in LDS; nobody reads the other buffer any more
-    if (t + 1 < tiles.n) {
-      const int k1 = tiles.key0(t + 1, KB);
-      KT::template load<kNT>(kbase, p.ks.token, k1, m.nk - 1, sm[(t + 1) & 1][0], wave, lane);
-      KT::template load<kNT>(vbase, p.vs.token, k1, m.nk - 1, sm[(t + 1) & 1][1], wave, lane);
-    }
-    const int k0 = tiles.key0(t, KB);
-    if (m.none(pw0, pw1, k0, k0 + KB - 1)) continue;
-    const char *ks = sm[t & 1][0], *vs = sm[t & 1][1];
-    v16f s[NB];
+  over_tiles<SPLIT>(
+      tiles.n,
+      [&](int t, int buf) {
+        const int k0 = tiles.key0(t, KB);
+        KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
+        KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
+      },
+      [&](int t, int buf) {
+        const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0, k1 = k0 + 32 * NB - 1;
+        if (i0 >= p.Lq || m.none(pw0, pw1, k0, k1)) return;
+        const char *ks = sm[buf][0], *vs = sm[buf][1];
+        v16f s[NB];
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb) {
-      s[kb] = v16f{};
+        for (int kb = 0; kb < NB; ++kb) {
+          s[kb] = v16f{};
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) s[kb] = mma(KT::row(ks, 32 * kb + n, kk, hi), q[kk], s[kb]);
-    }
-    if (!m.all(pw0, pw1, k0, k0 + KB - 1)) {
+          for (int kk = 0; kk < KK; ++kk) s[kb] = mma(KT::row(ks, r0 + 32 * kb + n, kk, hi), q[kk], s[kb]);
+        }
+        if (!m.all(pw0, pw1, k0, k1)) {
 #pragma unroll
-      for (int kb = 0; kb < NB; ++kb)
+          for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!m.sees(pos, k0 + 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3))) s[kb][r] = -INFINITY;
-    }
-    float mx = s[0][0];
+            for (int r = 0; r < 16; ++r)
+              if (!m.sees(pos, k0 + 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3))) s[kb][r] = -INFINITY;
+        }
+        float mx = s[0][0];
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb)
+        for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb][r]);
-    const float now = fmaxf(top, pair_max(mx) * sc);
-    const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - now);
-    const float ref = now == -INFINITY ? 0.f : now;  // (a row that has seen nothing: every weight is 0)
-    top = now;
-    l *= keep;
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb][r]);
+        const float now = fmaxf(top, pair_max(mx) * sc);
+        const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - now);
+        const float ref = now == -INFINITY ? 0.f : now;  // (a row that has seen nothing: every weight is 0)
+        top = now;
+        l *= keep;
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb)
+        for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[kb][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], sc, -ref));
-        l += s[kb][r];
-      }
+          for (int r = 0; r < 16; ++r) {
+            s[kb][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][r], sc, -ref));
+            l += s[kb][r];
+          }
 #pragma unroll
-    for (int d = 0; d < DB; ++d) o[d] *= keep;
+        for (int d = 0; d < DB; ++d) o[d] *= keep;
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb)
+        for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Frag<T> w8 = as_operand<T>(s[kb], h);
+          for (int h = 0; h < 2; ++h) {
+            const Frag<T> w8 = as_operand<T>(s[kb], h);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = mma(KT::col(vs, 32 * kb + 16 * h, d, lane), w8, o[d]);
-      }
-  }
+            for (int d = 0; d < DB; ++d) o[d] = mma(KT::col(vs, r0 + 32 * kb + 16 * h, d, lane), w8, o[d]);
+          }
+      });
   l = pair_sum(l);
+  if constexpr (SPLIT) {
+    // the waves' sums over the common maximum
+    __shared__ float tops[kWaves][32], sums[kWaves][32];
+    if (hi == 0) tops[wave][n] = top, sums[wave][n] = l;
+    __syncthreads();
+    float all = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) all = fmaxf(all, tops[x][n]);
+    const float ref = all == -INFINITY ? 0.f : all;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) sum = __builtin_fmaf(__builtin_amdgcn_exp2f(tops[x][n] - ref), sums[x][n], sum);
+    const float f = __builtin_amdgcn_exp2f(top - ref);
+#pragma unroll
+    for (int d = 0; d < DB; ++d) o[d] *= f;
+    top = all;
+    l = sum;
+    add_waves<D>(o, sm[0][0], wave, n, hi);
+    if (wave > 0) return;
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   if (__ballot(!all_finite<D>(o, inv) || l != l)) {
     fwd_by_pairs<T, D>(p, m, w.b, w.hk, w.h, i0, lane);
@@ -292,21 +373,25 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 }
 
 // ---------------------------------------------------------------------------
-// dq (and delta)
+// dq (and delta). delta = do . o uses the stored o; bfloat16 has rounded it,
+// which reaches ds = p (dp - delta) in full where few keys share the weight
+// (with one key ds is 0 for all do). With `exact` a first pass over the keys
+// forms delta = sum_j p_ij dp_ij instead.
 // ---------------------------------------------------------------------------
-template <typename T, int D>
+template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
-  constexpr int KB = kRows<T, D>, NB = KB / 32, KK = D / 16, DB = D / 32;
+  using Z = Shape<T, D, SPLIT>;
+  constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
-  __shared__ __attribute__((aligned(16))) char sm[2][2][KT::kBytes];
+  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][KT::kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, hi = lane >> 5;
   const Place<T> w = place_q(p);
   const Mask m = mask_of(p, w.b);
-  const int off = p.Lk - p.Lq, i0 = w.blk * kOwn + 32 * wave, i = i0 + n;
-  const int pos = i + off, pw0 = i0 + off, pw1 = pw0 + 31;
-  const int last_i = w.blk * kOwn + kOwn - 1 < p.Lq - 1 ? w.blk * kOwn + kOwn - 1 : p.Lq - 1;
-  const KeyTiles tiles(m, w.blk * kOwn + off, last_i + off, KB);
+  const int off = p.Lk - p.Lq, ib = w.blk * Z::kOwn, i0 = SPLIT ? ib : ib + 32 * wave, i = i0 + n;
+  const int pos = i + off, pw0 = i0 + off, pw1 = (i0 + 31 < p.Lq ? i0 + 31 : p.Lq - 1) + off;
+  const int last_i = ib + Z::kOwn < p.Lq ? ib + Z::kOwn - 1 : p.Lq - 1;
+  const KeyTiles tiles(m, ib + off, last_i + off, KB);
   const T* kbase = p.k + w.b * p.ks.batch + w.hk * p.ks.head;
   const T* vbase = p.v + w.b * p.vs.batch + w.hk * p.vs.head;
   const int ic = i < p.Lq ? i : p.Lq - 1;
@@ -326,56 +411,79 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
     }
   }
   delta = pair_sum(delta);
-  if (hi == 0 && i < p.Lq) p.delta[st] = delta;
   float lse = p.lse[st] * kLog2e;
   if (lse == -INFINITY) lse = 0.f;  // nothing seen: every weight is masked
   const float sc = p.scale * kLog2e;
   v16f dq[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dq[d] = v16f{};
-
-  if (tiles.n > 0) {
-    const int k0 = tiles.key0(0, KB);
-    KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[0][0], wave, lane);
-    KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[0][1], wave, lane);
-  }
-  for (int t = 0; t < tiles.n; ++t) {
-    wait_loads();
-    __syncthreads();
-    if (t + 1 < tiles.n) {
-      const int k1 = tiles.key0(t + 1, KB);
-      KT::template load<kNT>(kbase, p.ks.token, k1, m.nk - 1, sm[(t + 1) & 1][0], wave, lane);
-      KT::template load<kNT>(vbase, p.vs.token, k1, m.nk - 1, sm[(t + 1) & 1][1], wave, lane);
-    }
+  auto load = [&](int t, int buf) {
     const int k0 = tiles.key0(t, KB);
-    if (m.none(pw0, pw1, k0, k0 + KB - 1)) continue;
-    const bool full = m.all(pw0, pw1, k0, k0 + KB - 1);
-    const char *ks = sm[t & 1][0], *vs = sm[t & 1][1];
+    KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
+    KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
+  };
+  // weights and their gradients of one block of 32 keys (rows r0 .. of the tile)
+  auto scores = [&](int buf, int r0, int k0, v16f& s, v16f& dp) {
+    s = v16f{}, dp = v16f{};
 #pragma unroll
-    for (int kb = 0; kb < NB; ++kb) {
-      v16f s = v16f{}, dp = v16f{};
+    for (int kk = 0; kk < KK; ++kk) {
+      s = mma(KT::row(sm[buf][0], r0 + n, kk, hi), q[kk], s);
+      dp = mma(KT::row(sm[buf][1], r0 + n, kk, hi), go[kk], dp);
+    }
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        s = mma(KT::row(ks, 32 * kb + n, kk, hi), q[kk], s);
-        dp = mma(KT::row(vs, 32 * kb + n, kk, hi), go[kk], dp);
-      }
+    for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -lse));
+    if (!m.all(pw0, pw1, k0, k0 + 31)) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const float wt = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -lse));
-        s[r] = wt * (dp[r] - delta);
+        const bool seen = m.sees(pos, k0 + 8 * (r >> 2) + 4 * hi + (r & 3));
+        s[r] = seen ? s[r] : 0.f;
+        dp[r] = seen ? dp[r] : 0.f;
       }
-      if (!full) {
+    }
+  };
+  if (sizeof(T) == 2 && p.exact) {
+    float sum = 0.f;
+    over_tiles<SPLIT>(tiles.n, load, [&](int t, int buf) {
+      const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
+      if (i0 >= p.Lq) return;
+      for (int kb = 0; kb < NB; ++kb) {
+        if (m.none(pw0, pw1, k0 + 32 * kb, k0 + 32 * kb + 31)) continue;
+        v16f s, dp;
+        scores(buf, r0 + 32 * kb, k0 + 32 * kb, s, dp);
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (!m.sees(pos, k0 + 32 * kb + 8 * (r >> 2) + 4 * hi + (r & 3))) s[r] = 0.f;
+        for (int r = 0; r < 16; ++r) sum = __builtin_fmaf(s[r], dp[r], sum);
       }
+    });
+    sum = pair_sum(sum);
+    if constexpr (SPLIT) {
+      __shared__ float sums[kWaves][32];
+      if (hi == 0) sums[wave][n] = sum;
+      __syncthreads();
+      sum = (sums[0][n] + sums[1][n]) + (sums[2][n] + sums[3][n]);
+    }
+    delta = sum;
+  }
+  if (hi == 0 && i < p.Lq && (!SPLIT || wave == 0)) p.delta[st] = delta;
+  over_tiles<SPLIT>(tiles.n, load, [&](int t, int buf) {
+    const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
+    if (i0 >= p.Lq || m.none(pw0, pw1, k0, k0 + 32 * NB - 1)) return;
+#pragma unroll
+    for (int kb = 0; kb < NB; ++kb) {
+      v16f s, dp;
+      scores(buf, r0 + 32 * kb, k0 + 32 * kb, s, dp);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> ds = as_operand<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) dq[d] = mma(KT::col(ks, 32 * kb + 16 * h, d, lane), ds, dq[d]);
+        for (int d = 0; d < DB; ++d) dq[d] = mma(KT::col(sm[buf][0], r0 + 32 * kb + 16 * h, d, lane), ds, dq[d]);
       }
     }
+  });
+  if constexpr (SPLIT) {
+    add_waves<D>(dq, sm[0][0], wave, n, hi);
+    if (wave > 0) return;
   }
   if (__ballot(!all_finite<D>(dq, p.scale))) {
     __threadfence_block();  // delta, written by this wave, is read back
@@ -386,17 +494,19 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
 }
 
 // ---------------------------------------------------------------------------
-// dk and dv. SINK: the keys below S, 32 to a workgroup, whose waves take the
-// rows of the query tiles in turn and add their sums at the end; the
-// workgroups of a block of keys share the query tiles by ranges and leave
-// float32 partial sums.
+// dk and dv of the keys from S on, or (SINK) of those below S: every later
+// query sees these, so the workgroups of a block of 32 sinks share the query
+// tiles by ranges and leave float32 partial sums.
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool SINK>
+template <typename T, int D, bool SPLIT, bool SINK>
 __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
-  constexpr int QB = kRows<T, D>, NB = QB / 32, KK = D / 16, DB = D / 32;
+  static_assert(SPLIT || !SINK, "the sinks' workgroups share their keys");
+  using Z = Shape<T, D, SPLIT>;
+  constexpr int QB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using QT = Tile<T, D, QB>;
-  __shared__ __attribute__((aligned(16))) char sm[2][2][QT::kBytes];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][64];  // lse, delta of a tile's rows
+  constexpr int kStat = QB < 64 ? 64 : QB;
+  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][QT::kBytes];
+  __shared__ __attribute__((aligned(16))) float stat[Z::kBufs][2][kStat];  // lse, delta of a tile's rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, hi = lane >> 5;
   int w = SINK ? blockIdx.x : xcd_order(blockIdx.x, p.nwork);
@@ -409,18 +519,18 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
   w /= p.nblk;
   const int hk = w % p.Hk, b = w / p.Hk;
   const Mask m = mask_of(p, b);
-  const int off = p.Lk - p.Lq, j0 = SINK ? 32 * blk : blk * kOwn + 32 * wave, j = j0 + n;
+  const int off = p.Lk - p.Lq, jb = blk * Z::kOwn, jend = jb + Z::kOwn - 1;
+  const int j0 = SPLIT ? jb : jb + 32 * wave, j = j0 + n;
   // the queries that may see the workgroup's keys, by tiles
-  const int jb = SINK ? j0 : blk * kOwn, jend = SINK ? j0 + 31 : jb + kOwn - 1;
   const int ilo = jb - off > 0 ? jb - off : 0;
   const int64_t far = SINK ? p.Lq - 1 : static_cast<int64_t>(jend) + p.W - 1 - off;
   const int ihi = far < p.Lq - 1 ? static_cast<int>(far) : p.Lq - 1;
   const int t0 = ilo / QB, nt = m.nk > jb && ihi >= ilo && (SINK || jend >= p.S) ? ihi / QB - t0 + 1 : 0;
   int first = 0, end = nt * p.G;  // (head of the group, tile), flattened
   if (SINK) {
-    const int all = end;
-    first = static_cast<int>(static_cast<int64_t>(all) * chunk / p.nchunk);
-    end = static_cast<int>(static_cast<int64_t>(all) * (chunk + 1) / p.nchunk);
+    const int64_t all = end;
+    first = static_cast<int>(all * chunk / p.nchunk);
+    end = static_cast<int>(all * (chunk + 1) / p.nchunk);
   }
 
   Frag<T> k[KK], v[KK];
@@ -439,72 +549,75 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
 #pragma unroll
   for (int d = 0; d < DB; ++d) dk[d] = v16f{}, dv[d] = v16f{};
 
-  auto load = [&](int f, int buf) {
-    const int h = hk * p.G + f / nt, i0 = (t0 + f % nt) * QB;
-    QT::template load<kNT>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[buf][0], wave, lane);
-    QT::template load<kNT>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D, i0,
-                           p.Lq - 1, sm[buf][1], wave, lane);
-    if (wave < 2) {
-      const int i = i0 + lane < p.Lq - 1 ? i0 + lane : p.Lq - 1;
-      const float* src = (wave ? p.delta : p.lse) + (static_cast<int64_t>(b) * p.Hq + h) * p.Lq + i;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)stat[buf][wave], 4, 0, 0);
-    }
-  };
-  if (first < end) load(first, 0);
-  for (int f = first; f < end; ++f) {
-    const int cur = (f - first) & 1;
-    wait_loads();
-    __syncthreads();
-    if (f + 1 < end) load(f + 1, cur ^ 1);
-    const int i0 = (t0 + f % nt) * QB;
-    const char *qs = sm[cur][0], *gs = sm[cur][1];
+  over_tiles<SPLIT>(
+      end - first,
+      [&](int f, int buf) {
+        const int h = hk * p.G + (first + f) / nt, i0 = (t0 + (first + f) % nt) * QB;
+        QT::template load<kNT>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[buf][0], wave, lane);
+        QT::template load<kNT>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D,
+                               i0, p.Lq - 1, sm[buf][1], wave, lane);
+        const int part = wave >> 1;  // 64 rows of one of the two, a wave each
+        if (64 * part < kStat) {
+          const int i = i0 + 64 * part + lane < p.Lq ? i0 + 64 * part + lane : p.Lq - 1;
+          load_word_to_lds((wave & 1 ? p.delta : p.lse) + (static_cast<int64_t>(b) * p.Hq + h) * p.Lq,
+                           static_cast<unsigned>(i) * 4u, lds_address(&stat[buf][wave & 1][64 * part]));
+        }
+      },
+      [&](int f, int buf) {
+        const char *qs = sm[buf][0], *gs = sm[buf][1];
 #pragma unroll
-    for (int rb = 0; rb < NB; ++rb) {
-      const int ib = i0 + 32 * rb;
-      if (SINK && ((f - first) * NB + rb) % kWaves != wave) continue;
-      const int pb0 = ib + off, pb1 = pb0 + 31;
-      if (ib >= p.Lq || m.none(pb0, pb1, j0, j0 + 31)) continue;
-      v16f s = v16f{}, dp = v16f{};
+        for (int rb = 0; rb < NB; ++rb) {
+          const int r0 = SPLIT ? 32 * wave : 32 * rb;
+          const int ib = (t0 + (first + f) % nt) * QB + r0;
+          const int pb0 = ib + off, pb1 = pb0 + 31;
+          if (ib >= p.Lq || m.none(pb0, pb1, j0, j0 + 31)) continue;
+          v16f s = v16f{}, dp = v16f{};
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        s = mma(QT::row(qs, 32 * rb + n, kk, hi), k[kk], s);
-        dp = mma(QT::row(gs, 32 * rb + n, kk, hi), v[kk], dp);
-      }
-      const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq && (SINK ? j0 + 31 < p.S : j0 >= p.S);
-#pragma unroll
-      for (int r4 = 0; r4 < 4; ++r4) {
-        const float4 ls = *reinterpret_cast<const float4*>(&stat[cur][0][32 * rb + 8 * r4 + 4 * hi]);
-        const float4 de = *reinterpret_cast<const float4*>(&stat[cur][1][32 * rb + 8 * r4 + 4 * hi]);
-        const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dl[4] = {de.x, de.y, de.z, de.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int r = 4 * r4 + c;
-          float wt = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -lv[c] * kLog2e));
-          float ds = wt * (dp[r] - dl[c]);
-          if (!full) {
-            const int i = ib + 8 * r4 + 4 * hi + c;
-            const bool seen = i < p.Lq && m.sees(i + off, j) && (SINK ? j < p.S : j >= p.S);
-            wt = seen ? wt : 0.f;
-            ds = seen ? ds : 0.f;
+          for (int kk = 0; kk < KK; ++kk) {
+            s = mma(QT::row(qs, r0 + n, kk, hi), k[kk], s);
+            dp = mma(QT::row(gs, r0 + n, kk, hi), v[kk], dp);
           }
-          s[r] = wt;
-          dp[r] = ds;
-        }
-      }
+          const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq && (SINK ? j0 + 31 < p.S : j0 >= p.S);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Frag<T> wt = as_operand<T>(s, h), ds = as_operand<T>(dp, h);
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const float4 ls = *reinterpret_cast<const float4*>(&stat[buf][0][r0 + 8 * r4 + 4 * hi]);
+            const float4 de = *reinterpret_cast<const float4*>(&stat[buf][1][r0 + 8 * r4 + 4 * hi]);
+            const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dl[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          dv[d] = mma(QT::col(gs, 32 * rb + 16 * h, d, lane), wt, dv[d]);
-          dk[d] = mma(QT::col(qs, 32 * rb + 16 * h, d, lane), ds, dk[d]);
+            for (int c = 0; c < 4; ++c) {
+              const int r = 4 * r4 + c;
+              s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -lv[c] * kLog2e));
+              dp[r] = s[r] * (dp[r] - dl[c]);
+            }
+          }
+          if (!full) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+              const int i = ib + 8 * (r >> 2) + 4 * hi + (r & 3);
+              const bool seen = (i < p.Lq) & m.sees(i + off, j) & (SINK ? j < p.S : j >= p.S);
+              s[r] = seen ? s[r] : 0.f;
+              dp[r] = seen ? dp[r] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const Frag<T> wt = as_operand<T>(s, h), ds = as_operand<T>(dp, h);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              dv[d] = mma(QT::col(gs, r0 + 16 * h, d, lane), wt, dv[d]);
+              dk[d] = mma(QT::col(qs, r0 + 16 * h, d, lane), ds, dk[d]);
+            }
+          }
         }
-      }
-    }
+      });
+  if constexpr (SPLIT) {
+    add_waves<D>(dk, sm[0][0], wave, n, hi);
+    add_waves<D>(dv, sm[0][0], wave, n, hi);
+    if (wave > 0) return;
   }
+  const bool bad = __ballot(!all_finite<D>(dk, p.scale) || !all_finite<D>(dv, 1.f)) != 0;
   if constexpr (!SINK) {
-    if (__ballot(!all_finite<D>(dk, p.scale) || !all_finite<D>(dv, 1.f))) {
+    if (bad) {
       dkdv_by_pairs<T, D>(p, m, b, hk, j0, lane);
       return;
     }
@@ -514,41 +627,23 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
       store_col<T, D>(p.dv + o, dv, 1.f, hi);
     }
   } else {
-    // the four waves' sums, in wave order, through LDS (32 x D float32, dk then dv)
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 64 * D;
-    float* acc = reinterpret_cast<float*>(&sm[0][0][0]);  // [2][32][D]: at most 32 KiB of the tiles' 64
-    for (int x = 0; x < kWaves; ++x) {
-      __syncthreads();
-      if (wave == x)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int e = 32 * d + 8 * (r >> 2) + 4 * hi + (r & 3);
-            float* a = acc + n * D + e;
-            a[0] = x ? a[0] + dk[d][r] : dk[d][r];
-            a[32 * D] = x ? a[32 * D] + dv[d][r] : dv[d][r];
-          }
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 64 * D;  // dk, dv of 32 keys
+    if (!bad) {
+      store_col<float, D>(part + n * D, dk, 1.f, hi);
+      store_col<float, D>(part + (32 + n) * D, dv, 1.f, hi);
+      return;
     }
-    __syncthreads();
-    bool bad = false;
-    for (int e = threadIdx.x; e < 64 * D; e += kNT) {
-      bad = bad || !finite(acc[e]);
-      part[e] = acc[e];
-    }
-    if (__syncthreads_or(bad)) {
-      for (int c = wave; c < 32 && j0 + c < p.S && j0 + c < p.Lk; c += kWaves) {
-        Lane<T, D> sk, sv;
-        if (j0 + c < m.nk)
-          for (int f = first; f < end; ++f) {
-            const int i = (t0 + f % nt) * QB;
-            dkdv_pairs<T, D>(p, m, b, hk, hk * p.G + f / nt, j0 + c, i, i + QB < p.Lq ? i + QB : p.Lq, lane, sk, sv);
-          }
-#pragma unroll
-        for (int e = 0; e < D / 64; ++e) {
-          part[c * D + 64 * e + lane] = sk.v[e];
-          part[(32 + c) * D + 64 * e + lane] = sv.v[e];
+    for (int c = 0; c < 32 && j0 + c < p.S && j0 + c < p.Lk; ++c) {
+      Lane<T, D> sk, sv;
+      if (j0 + c < m.nk)
+        for (int f = first; f < end; ++f) {
+          const int i = (t0 + f % nt) * QB;
+          dkdv_pairs<T, D>(p, m, b, hk, hk * p.G + f / nt, j0 + c, i, i + QB < p.Lq ? i + QB : p.Lq, lane, sk, sv);
         }
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        part[c * D + 64 * e + lane] = sk.v[e];
+        part[(32 + c) * D + 64 * e + lane] = sv.v[e];
       }
     }
   }
@@ -575,6 +670,11 @@ __global__ __launch_bounds__(256) void swa_sink_join_kernel(const SwaArgs<T> p, 
 // host
 // ---------------------------------------------------------------------------
 constexpr int64_t kMostL = 1 << 30;
+constexpr int64_t kTogether = 256;
+// bfloat16: windows up to this take the exact delta. Wider ones spread the
+// weight: the rounding of o then reaches delta divided by the root of the
+// number of keys that share it.
+constexpr int64_t kExactWindow = 64;
 
 struct SwaSizes {
   int64_t nq, nk;  // elements of q and of k
@@ -616,12 +716,23 @@ SwaArgs<T> swa_args(const void* q, ssm_strides qs, const void* k, ssm_strides ks
 }
 
 // Workgroups that share a block of 32 sinks: about two for each compute unit
-// over all blocks, at least eight query tiles each.
+// over all blocks, at least two query tiles each.
 int sink_chunks(int64_t Bs, int64_t Lq, int64_t Hq, int64_t Hk, int64_t blocks) {
-  const int64_t tiles = (Lq + 63) / 64 * (Hq / Hk);
+  const int64_t tiles = (Lq + 127) / 128 * (Hq / Hk);
   const int64_t want = 512 / std::max<int64_t>(1, Bs * Hk * blocks);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, tiles / 8)));
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, tiles / 2)));
 }
+
+// Blocks of `own` rows over heads of L rows, as p.nblk and p.nwork.
+template <typename T>
+void set_blocks(SwaArgs<T>* a, int64_t Bs, int64_t heads, int64_t L, int own) {
+  a->nblk = static_cast<int>((L + own - 1) / own);
+  a->nwork = static_cast<int>(Bs * heads * a->nblk);
+}
+
+// Whether the waves of a workgroup work together on 32 rows: when workgroups
+// of 128 rows would not fill the compute units.
+bool together(int64_t Bs, int64_t heads, int64_t L) { return Bs * heads * ((L + 127) / 128) < kTogether; }
 
 int64_t sink_blocks(int64_t sinks, int64_t Lk) { return (std::min(sinks, Lk) + 31) / 32; }
 
@@ -647,18 +758,24 @@ extern "C" int ssm_swa_fwd(const void* q, const ssm_strides* qs, const void* k, 
   if ((rc = check_bufs(bufs, 6)) != SSM_OK) return rc;
   if (z.nq == 0) return SSM_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  auto go = [&](auto tag) {
+  auto go = [&](auto tag, auto dim) {
     using T = decltype(tag);
+    constexpr int DD = decltype(dim)::value;
     SwaArgs<T> a = swa_args<T>(q, sq, k, sk, v, sv, lens, Lq, Lk, Hq, Hk, window, sinks, scale);
     a.out = static_cast<T*>(o), a.lse = lse;
-    a.nblk = static_cast<int>((Lq + kOwn - 1) / kOwn), a.nwork = static_cast<int>(Bs * Hq * a.nblk);
-    if (D == 64)
-      hipLaunchKernelGGL((swa_fwd_kernel<T, 64>), dim3(a.nwork), dim3(kNT), 0, st, a);
-    else
-      hipLaunchKernelGGL((swa_fwd_kernel<T, 128>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    if (together(Bs, Hq, Lq)) {
+      set_blocks(&a, Bs, Hq, Lq, 32);
+      hipLaunchKernelGGL((swa_fwd_kernel<T, DD, true>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    } else {
+      set_blocks(&a, Bs, Hq, Lq, 128);
+      hipLaunchKernelGGL((swa_fwd_kernel<T, DD, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
   };
-  return dtype == SSM_F32 ? go(float{}) : go(uint16_t{});
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dtype == SSM_F32) return D == 64 ? go(float{}, D64{}) : go(float{}, D128{});
+  return D == 64 ? go(uint16_t{}, D64{}) : go(uint16_t{}, D128{});
 }
 
 extern "C" size_t ssm_swa_bwd_workspace_bytes(int64_t Bs, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hk, int64_t D,
@@ -706,17 +823,28 @@ extern "C" int ssm_swa_bwd(const void* q, const ssm_strides* qs, const void* k, 
     a.dq = static_cast<T*>(dq), a.dk = static_cast<T*>(dk), a.dv = static_cast<T*>(dv);
     a.delta = static_cast<float*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + stat_bytes(Bs, Lq, Hq));
-    a.nblk = static_cast<int>((Lq + kOwn - 1) / kOwn), a.nwork = static_cast<int>(Bs * Hq * a.nblk);
-    hipLaunchKernelGGL((swa_dq_kernel<T, DD>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    a.exact = window <= kExactWindow;
+    if (together(Bs, Hq, Lq)) {
+      set_blocks(&a, Bs, Hq, Lq, 32);
+      hipLaunchKernelGGL((swa_dq_kernel<T, DD, true>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    } else {
+      set_blocks(&a, Bs, Hq, Lq, 128);
+      hipLaunchKernelGGL((swa_dq_kernel<T, DD, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
+    }
     if (sinks < Lk) {
-      a.nblk = static_cast<int>((Lk + kOwn - 1) / kOwn), a.nwork = static_cast<int>(Bs * Hk * a.nblk);
-      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
+      if (together(Bs, Hk, Lk)) {
+        set_blocks(&a, Bs, Hk, Lk, 32);
+        hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
+      } else {
+        set_blocks(&a, Bs, Hk, Lk, 128);
+        hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, false, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
+      }
     }
     if (sinks > 0) {
       const int64_t nb = sink_blocks(sinks, Lk);
       a.nblk = static_cast<int>(nb), a.nchunk = sink_chunks(Bs, Lq, Hq, Hk, nb);
       a.nwork = static_cast<int>(Bs * Hk * nb * a.nchunk);
-      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true>), dim3(a.nwork), dim3(kNT), 0, st, a);
+      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true, true>), dim3(a.nwork), dim3(kNT), 0, st, a);
       const int64_t items = Bs * std::min(sinks, Lk) * Hk * 2 * D;
       hipLaunchKernelGGL((swa_sink_join_kernel<T>), dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, st,
                          a, static_cast<int>(Bs), static_cast<int>(D));

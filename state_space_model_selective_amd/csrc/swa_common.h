@@ -92,6 +92,30 @@ __device__ __forceinline__ float pair_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+__device__ __forceinline__ unsigned lds_address(const void* p) {
+  return static_cast<unsigned>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)(p)));
+}
+// 16 bytes a lane from base + off to LDS at `to` + 16 lane (base and `to` the same in the whole wave).
+__device__ __forceinline__ void load_to_lds(const char* base, unsigned off, unsigned to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(to), "v"(off), "s"(base)
+      : "memory", "m0");
+}
+
+__device__ __forceinline__ void load_word_to_lds(const float* base, unsigned off, unsigned to) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
+      : "s"(to), "v"(off), "s"(base)
+      : "memory", "m0");
+}
+
 // ---------------------------------------------------------------------------
 // An LDS tile of ROWS rows of D entries, in 16-byte chunks. Chunk c of row r
 // lies at position c ^ swizzle(r) of its row, so that 16 lanes on 16 rows
@@ -113,22 +137,25 @@ struct Tile {
 
   // Rows row0 .. row0 + ROWS - 1 (those past `last` read row `last` instead,
   // so that no row outside the valid ones is ever read; last >= row0). Each of
-  // the workgroup's NT threads moves chunks; the caller waits for vmcnt(0).
+  // the workgroup's NT threads moves chunks; the caller waits for vmcnt(0)
+  // before anyone reads them. (The loads are written in assembly because the
+  // compiler cannot tell the two buffers of a double-buffered tile apart: it
+  // waits for every load to LDS in flight before the next LDS read. They have
+  // no destination register; their addresses are read at issue.)
   template <int NT>
   static __device__ __forceinline__ void load(const T* base, int64_t stride, int row0, int last, char* lds, int wave,
                                               int lane) {
     static_assert(ROWS * kCpr % NT == 0, "whole passes");
     const char* first = reinterpret_cast<const char*>(base + row0 * stride);
     const unsigned row_bytes = static_cast<unsigned>(stride * static_cast<int64_t>(sizeof(T)));
+    const unsigned most = static_cast<unsigned>(last - row0) * row_bytes;
+    const unsigned to = lds_address(lds) + wave * 1024;
 #pragma unroll
     for (int it = 0; it < ROWS * kCpr / NT; ++it) {
       const int id = it * NT + wave * 64 + lane;
       const int r = id / kCpr, c = (id % kCpr) ^ swizzle(r);
-      const int rr = row0 + r <= last ? r : last - row0;
-      const unsigned off = static_cast<unsigned>(rr) * row_bytes + static_cast<unsigned>(c) * 16u;
-      char* dst = lds + (it * NT + wave * 64) * 16;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(first + off),
-                                       (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
+      const unsigned at_row = static_cast<unsigned>(r) * row_bytes;
+      load_to_lds(first, (at_row < most ? at_row : most) + static_cast<unsigned>(c) * 16u, to + it * NT * 16);
     }
   }
 
@@ -171,7 +198,13 @@ struct Tile {
   }
 };
 
-__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Waits for the wave's outstanding loads (vmcnt(0), nothing else): the builtin,
+// which the compiler counts with, and a barrier to its reordering.
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);
+  asm volatile("" ::: "memory");
+}
 
 // ---------------------------------------------------------------------------
 // arguments, mask
@@ -196,6 +229,7 @@ struct SwaArgs {
   int nblk;      // blocks of queries (or keys) of a head
   int nwork;     // workgroups
   int nchunk;    // sinks: workgroups that share a block of keys
+  int exact;     // dq: form delta from the weights in a pass of its own
   float scale;
 };
 
@@ -203,7 +237,7 @@ struct SwaArgs {
 // row's key count, when j <= p and (p - j < W or j < S).
 struct Mask {
   int nk, W, S;
-  __device__ __forceinline__ bool sees(int p, int j) const { return j <= p && j < nk && (p - j < W || j < S); }
+  __device__ __forceinline__ bool sees(int p, int j) const { return (j <= p) & (j < nk) & ((p - j < W) | (j < S)); }
   // every position of [p0, p1] sees every key of [j0, j1]
   __device__ __forceinline__ bool all(int p0, int p1, int j0, int j1) const {
     return j1 <= p0 && j1 < nk && (p1 - j0 < W || j1 < S);
