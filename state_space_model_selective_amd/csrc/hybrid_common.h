@@ -52,19 +52,23 @@ struct Vec16<uint16_t> {
   }
 };
 
-// dst[c] = sum over rows of part (rows, cols), in a fixed order: 16 threads of
-// a column each sum every 16th row, their sums are added in thread order.
-__global__ __launch_bounds__(256) void sum_rows_kernel(const float* part, float* dst, int64_t rows, int64_t cols) {
-  __shared__ float sum[16][17];
+// dst[c] = sum over rows of part (rows, cols), in a fixed order: 64 threads of
+// a column each sum every 64th row, their sums are added in thread order. (One
+// thread a column would wait for a load a row.)
+[[maybe_unused]] __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* part, float* dst, int64_t rows,
+                                                                         int64_t cols) {
+  __shared__ float sum[64][17];
   const int ce = threadIdx.x & 15, cr = threadIdx.x >> 4;
   const int64_t e = blockIdx.x * 16ll + ce;
   float v = 0.f;
   if (e < cols)
-    for (int64_t r = cr; r < rows; r += 16) v += part[r * cols + e];
+#pragma unroll 8
+    for (int64_t r = cr; r < rows; r += 64) v += part[r * cols + e];
   sum[cr][ce] = v;
   __syncthreads();
   if (cr == 0 && e < cols) {
-    for (int j = 1; j < 16; ++j) v += sum[j][ce];
+#pragma unroll
+    for (int j = 1; j < 64; ++j) v += sum[j][ce];
     dst[e] = v;
   }
 }

@@ -3,11 +3,16 @@
 //   r = sigmoid(gr), i = sigmoid(gi), la = A r, a = e^la, s = sqrt(max(0, 1 - e^(2 la)))
 //   h_t = a_t h_{t-1} + s_t i_t x_t,   y_t = h_t
 //
-// A thread owns VEC neighbouring channels of one chunk of steps. A chunk's
-// effect on the state is the affine map h -> P h + H; a first kernel forms
-// (P, H) of every chunk, a second folds them along the sequence into the
-// state entering each chunk, the third runs every chunk from that state.
-// The backward does the same with the adjoint, in reverse time.
+// A run of steps takes the state through an affine map h -> P h + H. Forward,
+// one pass over the data: a wave forms the map of 16 steps and keeps every
+// step's part of it in registers, its workgroup joins eight of them to a chunk
+// of 128 steps, and chunks pass maps and states on through the workspace (see
+// Handoff); then every step's state follows from the one entering the wave.
+// Backward: the maps of the adjoint, chunk by chunk, their fold along the
+// sequence, then every chunk again from its entering adjoint, in blocks of 16
+// steps whose states start from the forward's checkpoints.
+#include <type_traits>
+
 #include "hybrid_common.h"
 
 namespace {
@@ -17,11 +22,69 @@ constexpr int kCk = SSM_GLR_CKPT_STEPS;
 // ---------------------------------------------------------------------------
 // VEC-wide element access
 // ---------------------------------------------------------------------------
+// A row's address kept in scalar registers: with a lane's 32-bit offset added
+// last, an access takes one vector register for its address and not two for
+// every row. (Device memory: the cast keeps the accesses global.)
+#define SSM_GLOBAL __attribute__((address_space(1)))
+template <typename P>
+__device__ __forceinline__ SSM_GLOBAL P* scalar(P* p) {
+  SSM_GLOBAL P* g = (SSM_GLOBAL P*)p;
+  asm("" : "+s"(g));
+  return g;
+}
+
+// the loaded bits, widened when they are used (a wave can then have many loads
+// in flight)
+template <typename T, int VEC>
+struct RawOf {
+  using type = T;
+};
+template <>
+struct RawOf<uint16_t, 2> {
+  using type = uint32_t;
+};
+template <>
+struct RawOf<float, 2> {
+  using type = float2;
+};
+template <typename T, int VEC>
+__device__ __forceinline__ typename RawOf<T, VEC>::type load_raw(const SSM_GLOBAL T* p) {
+  using Raw = typename RawOf<T, VEC>::type;
+  if constexpr (std::is_same<Raw, float2>::value) {
+    return make_float2(p[0], p[1]);
+  } else {
+    return *(const SSM_GLOBAL Raw*)p;
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_raw(SSM_GLOBAL T* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 2 && sizeof(T) == 2) {
+    *(SSM_GLOBAL uint32_t*)p = pack_bf16(v[0], v[1]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) p[c] = from_f32<T>(v[c]);
+  }
+}
+__device__ __forceinline__ void widen_pair(uint32_t r, float (&v)[2]) {
+  v[0] = __uint_as_float(r << 16), v[1] = __uint_as_float(r & 0xffff0000u);
+}
+__device__ __forceinline__ void widen_pair(float2 r, float (&v)[2]) { v[0] = r.x, v[1] = r.y; }
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(typename RawOf<T, VEC>::type r, float (&v)[VEC]) {
+  if constexpr (VEC == 2) {
+    widen_pair(r, v);
+  } else {
+    v[0] = to_f32(r);
+  }
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
   if constexpr (VEC == 4) {
     const float4 f = Vec4<T>::load(p);
     v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+  } else if constexpr (VEC == 2) {
+    widen_pair(*reinterpret_cast<const typename RawOf<T, 2>::type*>(p), v);
   } else {
     v[0] = to_f32(p[0]);
   }
@@ -30,6 +93,10 @@ template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   if constexpr (VEC == 4) {
     Vec4<T>::store(p, make_float4(v[0], v[1], v[2], v[3]));
+  } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(v[0], v[1]);
+  } else if constexpr (VEC == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
   } else {
     p[0] = from_f32<T>(v[0]);
   }
@@ -86,189 +153,419 @@ struct GlrArgs {
   T* dgr;
   T* dgi;
   float* dh0;
+  int64_t Bs, L, ED, ckrows;
+  // forward: the hand-off
+  unsigned* hdr;        // ticket
+  unsigned* flag;       // [chunk][group]: the chunk's map is there
+  unsigned* sflag;      // [span][group]: the state entering the span is there
+  uint64_t* map;        // [chunk][group][channel]: (P, H)
+  unsigned* state;      // [span][group][channel]
+  int64_t nchunks, ngroups, ncg;  // ncg: groups of 64 VEC channels of a row; ngroups = Bs ncg
+  unsigned spin_limit;
+  // backward
   float2* agg;     // (Bs, nchunks, ED): (P, H) of each chunk
-  float* enter;    // (Bs, nchunks, ED): the state (backward: the adjoint) entering each chunk
+  float* enter;    // (Bs, nchunks, ED): the adjoint entering each chunk
   float* dA_part;  // (Bs, nchunks, ED)
-  int64_t Bs, L, ED, ncg, nchunks, steps, ckrows;
+  int64_t steps;
 };
 
-// The chunk and channels of this thread; false past the end.
-template <typename T, int VEC>
-__device__ __forceinline__ bool place(const GlrArgs<T>& p, int64_t* b, int64_t* k, int64_t* e) {
-  const int64_t item = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (item >= p.Bs * p.nchunks * p.ncg) return false;
-  *e = (item % p.ncg) * VEC;
-  *k = (item / p.ncg) % p.nchunks;
-  *b = item / p.ncg / p.nchunks;
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+// Handoff between the chunks of a channel group. Chunks are dealt out by a
+// ticket, all groups' chunk k before any chunk k + 1, so whatever a chunk
+// waits for has been taken by a workgroup that runs. kSpan chunks make a
+// span. A chunk publishes its map at once (waiting for nothing), then needs
+// the maps of the chunks before it in its span and the state entering the
+// span, which the last chunk of the span before publishes. A chain of states
+// through all chunks would cost a trip between compute units each (about 2
+// us, 2 ms over 1024 chunks); here the chain has a step a span, and the maps
+// read in between are kSpan / 2 of 8 bytes a channel on average beside the
+// chunk's 128 steps. The order of every sum is fixed by the chunk's place.
+//   Maps, states and flags are written and read by agent-scope atomics, which
+// go past the caches that are not shared; a publisher waits for its stores
+// (vmcnt(0)) before it raises the flag. The wait is bounded: if it ever gives
+// up, the chunk takes NaN as its entering state.
+constexpr int kSpan = 16;
+constexpr int kFwdWaves = 8, kChunk = kFwdWaves * kCk;
+
+__device__ __forceinline__ void publish_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void put_flag(unsigned* f) {
+  __hip_atomic_store(f, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits until every lane's flag is raised (lanes with f == nullptr have none).
+__device__ __forceinline__ bool wait_flags(const unsigned* f, unsigned limit) {
+  bool there = !f;
+  for (unsigned it = 0;; ++it) {
+    if (!there) there = __hip_atomic_load(f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0;
+    if (__all(there)) break;
+    if (it >= limit) return false;
+    __builtin_amdgcn_s_sleep(1);
+  }
+  asm volatile("" ::: "memory");
   return true;
 }
 
+// body(true) for a whole block of kCk steps, body(false) for the sequence's last.
+template <typename F>
+__device__ __forceinline__ void run_steps(int m, F body) {
+  if (m == kCk)
+    body(std::integral_constant<bool, true>{});
+  else
+    body(std::integral_constant<bool, false>{});
+}
+
+// Chunk, group, batch row and channel group of a work item. (A division runs on
+// the vector unit; the results go back to scalars so that addresses do too.)
+template <typename T>
+__device__ __forceinline__ void locate(const GlrArgs<T>& p, unsigned item, int64_t* k, int64_t* group, int64_t* b,
+                                       int64_t* cg) {
+  const unsigned ng = static_cast<unsigned>(p.ngroups), nc = static_cast<unsigned>(p.ncg);
+  const unsigned kk = __builtin_amdgcn_readfirstlane(item / ng), g = item - kk * ng;
+  const unsigned bb = __builtin_amdgcn_readfirstlane(g / nc);
+  *k = kk, *group = g, *b = bb, *cg = g - bb * nc;
+}
+
+// What the loads cannot do without: 3 inputs and 1 output of an element;
+// the gates cost about 25 vector and 6 transcendental instructions each.
 template <typename T, int VEC>
-__global__ __launch_bounds__(256) void glr_agg_kernel(const GlrArgs<T> p) {
-  int64_t b, k, e;
-  if (!place<T, VEC>(p, &b, &k, &e)) return;
-  const int64_t t0 = k * p.steps, n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
-  int64_t at = (b * p.L + t0) * p.ED + e;
-  float A2[VEC], P[VEC], H[VEC];
+__global__ __launch_bounds__(64 * kFwdWaves, 4) void glr_fwd_kernel(const GlrArgs<T> p) {
+  __shared__ float2 maps[kFwdWaves][64][VEC];
+  __shared__ float entering[64][VEC];
+  __shared__ unsigned s_ticket;
+  using Raw = typename RawOf<T, VEC>::type;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  unsigned item = blockIdx.x;
+  if (p.nchunks > 1) {
+    if (threadIdx.x == 0) s_ticket = __hip_atomic_fetch_add(p.hdr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    item = __builtin_amdgcn_readfirstlane(s_ticket);
+  }
+  int64_t k, group, b, cg;
+  locate(p, item, &k, &group, &b, &cg);
+  const int64_t e = cg * 64 * VEC + lane * VEC;
+  const bool ok = e < p.ED;  // (ED is a multiple of VEC)
+  const unsigned lo = ok ? lane * VEC : 0;  // the lane's channel after the group's first
+  const int64_t t0 = k * kChunk + wave * kCk, left = p.L - t0;
+  const int m = left < 0 ? 0 : left < kCk ? static_cast<int>(left) : kCk;  // steps of this wave
+  const int64_t at = (b * p.L + t0) * p.ED + cg * 64 * VEC;
+
+  float P[VEC], H[VEC], Pt[kCk][VEC], Ht[kCk][VEC];
+  run_steps(m, [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    Raw xr[kCk], rr[kCk], ir[kCk];
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) A2[c] = p.A[e + c] * kLog2e, P[c] = 1.f, H[c] = 0.f;
-#pragma unroll 4
-  for (int64_t t = 0; t < n; ++t, at += p.ED) {
-    float x[VEC], gr[VEC], gi[VEC];
-    load_vec<T, VEC>(p.x + at, x);
-    load_vec<T, VEC>(p.gr + at, gr);
-    load_vec<T, VEC>(p.gi + at, gi);
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) {
+        xr[t] = load_raw<T, VEC>(scalar(p.x + at + t * p.ED) + lo);
+        rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + lo);
+        ir[t] = load_raw<T, VEC>(scalar(p.gi + at + t * p.ED) + lo);
+      }
+    float A2[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) A2[c] = p.A[cg * 64 * VEC + lo + c] * kLog2e, P[c] = 1.f, H[c] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) {
+        float x[VEC], gr[VEC], gi[VEC];
+        widen<T, VEC>(xr[t], x);
+        widen<T, VEC>(rr[t], gr);
+        widen<T, VEC>(ir[t], gi);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const Gates g = gates(gr[c], gi[c], A2[c]);
+          P[c] *= g.a;
+          H[c] = __builtin_fmaf(g.a, H[c], g.s * g.i * x[c]);
+          Pt[t][c] = P[c];
+          Ht[t][c] = H[c];
+        }
+      }
+  });
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) maps[wave][lane][c] = make_float2(P[c], H[c]);
+  __syncthreads();
+  if (wave == 0) {
+    float h[VEC];
+    float cp[VEC], ch[VEC];  // the chunk's map
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      const Gates g = gates(gr[c], gi[c], A2[c]);
-      P[c] *= g.a;
-      H[c] = __builtin_fmaf(g.a, H[c], g.s * g.i * x[c]);
+      cp[c] = 1.f, ch[c] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kFwdWaves; ++w) {
+        const float2 v = maps[w][lane][c];
+        cp[c] *= v.x;
+        ch[c] = __builtin_fmaf(v.x, ch[c], v.y);
+      }
+      h[c] = p.h0 && ok ? p.h0[b * p.ED + e + c] : 0.f;
+    }
+    if (p.nchunks > 1) {
+      const int64_t span = k / kSpan, cw = 64 * VEC, mine = lane * VEC;
+      const int place = static_cast<int>(k % kSpan);
+      const bool more = k + 1 < p.nchunks;
+      if (more && place < kSpan - 1) {
+        uint64_t* to = p.map + (k * p.ngroups + group) * cw + mine;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+          __hip_atomic_store(to + c, __builtin_bit_cast(uint64_t, make_float2(cp[c], ch[c])), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+        publish_fence();
+        if (lane == 0) put_flag(p.flag + k * p.ngroups + group);
+      }
+      // the maps before this chunk in its span, joined
+      bool good = wait_flags(lane < place ? p.flag + (span * kSpan + lane) * p.ngroups + group : nullptr, p.spin_limit);
+      float bp[VEC], bh[VEC];
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) bp[c] = 1.f, bh[c] = 0.f;
+#pragma unroll 5
+      for (int j = 0; j < place; ++j) {
+        uint64_t* from = p.map + ((span * kSpan + j) * p.ngroups + group) * cw + mine;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const float2 v = __builtin_bit_cast(float2, __hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+          bp[c] *= v.x;
+          bh[c] = __builtin_fmaf(v.x, bh[c], v.y);
+        }
+      }
+      if (span > 0) {
+        good = wait_flags(lane == 0 ? p.sflag + span * p.ngroups + group : nullptr, p.spin_limit) && good;
+        unsigned* from = p.state + (span * p.ngroups + group) * cw + mine;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+          h[c] = __uint_as_float(__hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+      }
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = good ? __builtin_fmaf(bp[c], h[c], bh[c]) : __builtin_nanf("");
+      if (more && place == kSpan - 1) {
+        unsigned* to = p.state + ((span + 1) * p.ngroups + group) * cw + mine;
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+          __hip_atomic_store(to + c, __float_as_uint(__builtin_fmaf(cp[c], h[c], ch[c])), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+        publish_fence();
+        if (lane == 0) put_flag(p.sflag + (span + 1) * p.ngroups + group);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      entering[lane][c] = h[c];
+      if (p.h_last && ok && k + 1 == p.nchunks) p.h_last[b * p.ED + e + c] = __builtin_fmaf(cp[c], h[c], ch[c]);
     }
   }
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) p.agg[(b * p.nchunks + k) * p.ED + e + c] = make_float2(P[c], H[c]);
-}
-
-// enter[k] = fold of the chunks before k (rev: after k) from `init`.
-__global__ __launch_bounds__(64) void glr_join_kernel(const float2* agg, const float* init, float* enter, int64_t n,
-                                                      int64_t nchunks, int64_t ED, int rev) {
-  const int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
-  if (i >= n) return;
-  const int64_t b = i / ED, e = i % ED;
-  float h = init ? init[i] : 0.f;
-#pragma unroll 8
-  for (int64_t j = 0; j < nchunks; ++j) {
-    const int64_t k = rev ? nchunks - 1 - j : j;
-    const int64_t o = (b * nchunks + k) * ED + e;
-    const float2 m = agg[o];
-    enter[o] = h;
-    h = __builtin_fmaf(m.x, h, m.y);
-  }
-}
-
-template <typename T, int VEC>
-__global__ __launch_bounds__(256) void glr_apply_kernel(const GlrArgs<T> p) {
-  int64_t b, k, e;
-  if (!place<T, VEC>(p, &b, &k, &e)) return;
-  const int64_t t0 = k * p.steps, n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
-  int64_t at = (b * p.L + t0) * p.ED + e;
-  float A2[VEC], h[VEC];
+  __syncthreads();
+  if (m == 0 || !ok) return;
+  float h[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
-    A2[c] = p.A[e + c] * kLog2e;
-    h[c] = p.enter ? p.enter[(b * p.nchunks + k) * p.ED + e + c] : p.h0 ? p.h0[b * p.ED + e + c] : 0.f;
-  }
-#pragma unroll 4
-  for (int64_t t = 0; t < n; ++t, at += p.ED) {
-    if (p.ckpt && (t0 + t) % kCk == 0) store_vec<float, VEC>(p.ckpt + (b * p.ckrows + (t0 + t) / kCk) * p.ED + e, h);
-    float x[VEC], gr[VEC], gi[VEC];
-    load_vec<T, VEC>(p.x + at, x);
-    load_vec<T, VEC>(p.gr + at, gr);
-    load_vec<T, VEC>(p.gi + at, gi);
+    h[c] = entering[lane][c];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      const Gates g = gates(gr[c], gi[c], A2[c]);
-      h[c] = __builtin_fmaf(g.a, h[c], g.s * g.i * x[c]);
-    }
-    store_vec<T, VEC>(p.y + at, h);
+    for (int w = 0; w < kFwdWaves - 1; ++w)
+      if (w < wave) {
+        const float2 v = maps[w][lane][c];
+        h[c] = __builtin_fmaf(v.x, h[c], v.y);
+      }
   }
-  if (p.h_last && k == p.nchunks - 1) store_vec<float, VEC>(p.h_last + b * p.ED + e, h);
+  if (p.ckpt) store_vec<float, VEC>(p.ckpt + (b * p.ckrows + t0 / kCk) * p.ED + e, h);
+  run_steps(m, [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+#pragma unroll
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) {
+        float y[VEC];
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) y[c] = __builtin_fmaf(Pt[t][c], h[c], Ht[t][c]);
+        store_raw<T, VEC>(scalar(p.y + at + t * p.ED) + lo, y);
+      }
+  });
 }
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+// enter[k] = the adjoint entering chunk k from the chunks after it and `init`.
+// 16 channels a workgroup; a channel's chunks are shared by 16 threads, which
+// join the maps of a run each, then walk their run from its entering adjoint.
+__global__ __launch_bounds__(256) void glr_join_kernel(const float2* agg, const float* init, float* enter,
+                                                       int64_t nchunks, int64_t ED, int64_t ncol) {
+  __shared__ float2 runs[16][16];
+  const int ce = threadIdx.x & 15, seg = threadIdx.x >> 4;
+  const int64_t b = blockIdx.x / ncol, e = (blockIdx.x % ncol) * 16 + ce;
+  const bool ok = e < ED;
+  // run `seg` of the reversed order: chunks hi - 1 down to lo
+  const int64_t hi = nchunks - nchunks * seg / 16, lo = nchunks - nchunks * (seg + 1) / 16;
+  const int64_t at = b * nchunks * ED + e;
+  float P = 1.f, H = 0.f;
+  if (ok)
+#pragma unroll 8
+    for (int64_t k = hi - 1; k >= lo; --k) {
+      const float2 m = agg[at + k * ED];
+      P *= m.x;
+      H = __builtin_fmaf(m.x, H, m.y);
+    }
+  runs[seg][ce] = make_float2(P, H);
+  __syncthreads();
+  if (!ok) return;
+  float g = init ? init[b * ED + e] : 0.f;
+  for (int s = 0; s < seg; ++s) g = __builtin_fmaf(runs[s][ce].x, g, runs[s][ce].y);
+#pragma unroll 8
+  for (int64_t k = hi - 1; k >= lo; --k) {
+    const float2 m = agg[at + k * ED];
+    enter[at + k * ED] = g;
+    g = __builtin_fmaf(m.x, g, m.y);
+  }
+}
+
+// A wave's chunk and its group of 64 VEC channels; false past the end.
+template <typename T, int VEC>
+struct BwdPlace {
+  int64_t b, k, e0, t0, n;  // first channel, first step, steps
+  unsigned lo;              // the lane's channel after e0
+  bool ok;
+  __device__ __forceinline__ bool find(const GlrArgs<T>& p) {
+    const int lane = threadIdx.x & 63;
+    const unsigned item = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (item >= p.ngroups * p.nchunks) return false;
+    int64_t group, cg;
+    locate(p, item, &k, &group, &b, &cg);
+    e0 = cg * 64 * VEC;
+    ok = e0 + lane * VEC < p.ED;
+    lo = ok ? lane * VEC : 0;
+    t0 = k * p.steps;
+    n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
+    return true;
+  }
+  // of an array (Bs, nchunks, ED)
+  __device__ __forceinline__ int64_t slot(const GlrArgs<T>& p) const { return (b * p.nchunks + k) * p.ED + e0 + lo; }
+};
 
 // The adjoint's aggregate of a chunk: G -> P G + H with G entering after the
 // chunk's last step and leaving before its first (a_t applied).
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void glr_bwd_agg_kernel(const GlrArgs<T> p) {
-  int64_t b, k, e;
-  if (!place<T, VEC>(p, &b, &k, &e)) return;
-  const int64_t t0 = k * p.steps, n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
-  int64_t at = (b * p.L + t0 + n - 1) * p.ED + e;
+  using Raw = typename RawOf<T, VEC>::type;
+  BwdPlace<T, VEC> w;
+  if (!w.find(p)) return;
   float A2[VEC], P[VEC], H[VEC];
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) A2[c] = p.A[e + c] * kLog2e, P[c] = 1.f, H[c] = 0.f;
-#pragma unroll 4
-  for (int64_t t = 0; t < n; ++t, at -= p.ED) {
-    float gr[VEC], dy[VEC];
-    load_vec<T, VEC>(p.gr + at, gr);
-    load_vec<T, VEC>(p.dy + at, dy);
+  for (int c = 0; c < VEC; ++c) A2[c] = p.A[w.e0 + w.lo + c] * kLog2e, P[c] = 1.f, H[c] = 0.f;
+  for (int64_t blk = (w.n + kCk - 1) / kCk - 1; blk >= 0; --blk) {
+    const int m = static_cast<int>(w.n - blk * kCk < kCk ? w.n - blk * kCk : kCk);
+    const int64_t at = (w.b * p.L + w.t0 + blk * kCk) * p.ED + w.e0;
+    run_steps(m, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      Raw rr[kCk], dr[kCk];
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      const float a = __builtin_amdgcn_exp2f(A2[c] * sigmoid_fast(gr[c]));
-      P[c] *= a;
-      H[c] = a * (H[c] + dy[c]);
-    }
+      for (int t = kCk - 1; t >= 0; --t)
+        if (FULL || t < m) {
+          rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + w.lo);
+          dr[t] = load_raw<T, VEC>(scalar(p.dy + at + t * p.ED) + w.lo);
+        }
+#pragma unroll
+      for (int t = kCk - 1; t >= 0; --t)
+        if (FULL || t < m) {
+          float gr[VEC], dy[VEC];
+          widen<T, VEC>(rr[t], gr);
+          widen<T, VEC>(dr[t], dy);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            const float a = __builtin_amdgcn_exp2f(A2[c] * sigmoid_fast(gr[c]));
+            P[c] *= a;
+            H[c] = a * (H[c] + dy[c]);
+          }
+        }
+    });
   }
+  if (w.ok)
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) p.agg[(b * p.nchunks + k) * p.ED + e + c] = make_float2(P[c], H[c]);
+    for (int c = 0; c < VEC; ++c) p.agg[w.slot(p) + c] = make_float2(P[c], H[c]);
 }
 
-// Blocks of kCk steps in reverse order: the states of the block again from
-// its checkpoint, then its adjoint steps backwards.
+// Blocks of kCk steps in reverse order. A block's gates are formed once, going
+// forwards from its checkpoint; what the way back needs of a step stays in
+// registers: a and the factors of g in dx, dgi, dla r and dgr.
 template <typename T, int VEC>
-__global__ __launch_bounds__(256) void glr_bwd_apply_kernel(const GlrArgs<T> p) {
-  int64_t b, k, e;
-  if (!place<T, VEC>(p, &b, &k, &e)) return;
-  const int64_t t0 = k * p.steps, n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
-  float A[VEC], A2[VEC], G[VEC], dA[VEC];
+__global__ __launch_bounds__(256, 2) void glr_bwd_apply_kernel(const GlrArgs<T> p) {
+  using Raw = typename RawOf<T, VEC>::type;
+  BwdPlace<T, VEC> w;
+  if (!w.find(p)) return;
+  float A[VEC], G[VEC], dA[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
-    A[c] = p.A[e + c];
-    A2[c] = A[c] * kLog2e;
+    A[c] = p.A[w.e0 + w.lo + c];
     dA[c] = 0.f;
-    G[c] = p.enter[(b * p.nchunks + k) * p.ED + e + c];
+    G[c] = p.enter[w.slot(p) + c];
   }
-  for (int64_t blk = (n + kCk - 1) / kCk - 1; blk >= 0; --blk) {
-    const int64_t tb = t0 + blk * kCk;
-    const int m = static_cast<int>(t0 + n - tb < kCk ? t0 + n - tb : kCk);
-    const int64_t at = (b * p.L + tb) * p.ED + e;
-    float hp[kCk][VEC], h[VEC];  // h_{t-1} of the block's steps
-    load_vec<float, VEC>(p.ckpt + (b * p.ckrows + tb / kCk) * p.ED + e, h);
+  for (int64_t blk = (w.n + kCk - 1) / kCk - 1; blk >= 0; --blk) {
+    const int64_t tb = w.t0 + blk * kCk;
+    const int m = static_cast<int>(w.n - blk * kCk < kCk ? w.n - blk * kCk : kCk);
+    const int64_t at = (w.b * p.L + tb) * p.ED + w.e0;
+    run_steps(m, [&](auto full) {
+      constexpr bool FULL = decltype(full)::value;
+      Raw xr[kCk], rr[kCk], ir[kCk], dr[kCk];
+      float h[VEC];
+      load_vec<float, VEC>(p.ckpt + (w.b * p.ckrows + tb / kCk) * p.ED + w.e0 + w.lo, h);
 #pragma unroll
-    for (int t = 0; t < kCk; ++t) {
-      if (t < m) {
-        float x[VEC], gr[VEC], gi[VEC];
-        load_vec<T, VEC>(p.x + at + t * p.ED, x);
-        load_vec<T, VEC>(p.gr + at + t * p.ED, gr);
-        load_vec<T, VEC>(p.gi + at + t * p.ED, gi);
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const Gates g = gates(gr[c], gi[c], A2[c]);
-          hp[t][c] = h[c];
-          h[c] = __builtin_fmaf(g.a, h[c], g.s * g.i * x[c]);
+      for (int t = 0; t < kCk; ++t)
+        if (FULL || t < m) {
+          xr[t] = load_raw<T, VEC>(scalar(p.x + at + t * p.ED) + w.lo);
+          rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + w.lo);
+          ir[t] = load_raw<T, VEC>(scalar(p.gi + at + t * p.ED) + w.lo);
         }
-      }
-    }
 #pragma unroll
-    for (int t = kCk - 1; t >= 0; --t) {
-      if (t < m) {
-        const int64_t o = at + t * p.ED;
-        float x[VEC], gr[VEC], gi[VEC], dy[VEC], dx[VEC], dgr[VEC], dgi[VEC];
-        load_vec<T, VEC>(p.x + o, x);
-        load_vec<T, VEC>(p.gr + o, gr);
-        load_vec<T, VEC>(p.gi + o, gi);
-        load_vec<T, VEC>(p.dy + o, dy);
+      for (int t = kCk - 1; t >= 0; --t)
+        if (FULL || t < m) dr[t] = load_raw<T, VEC>(scalar(p.dy + at + t * p.ED) + w.lo);
+      float fa[kCk][VEC], fx[kCk][VEC], fi[kCk][VEC], fl[kCk][VEC], fr[kCk][VEC];
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const Gates q = gates(gr[c], gi[c], A2[c]);
-          const float g = G[c] + dy[c];
-          const float ix = q.i * x[c], gs = g * q.s;
-          const float root = q.s > 0.f ? q.a * q.a * rcp_fast(q.s) * ix : 0.f;
-          const float dlr = g * (q.a * hp[t][c] - root) * q.r;  // dla r
-          dx[c] = gs * q.i;
-          dgi[c] = gs * ix * (1.f - q.i);
-          dgr[c] = dlr * A[c] * (1.f - q.r);
-          dA[c] += dlr;
-          G[c] = q.a * g;
+      for (int t = 0; t < kCk; ++t)
+        if (FULL || t < m) {
+          float x[VEC], gr[VEC], gi[VEC];
+          widen<T, VEC>(xr[t], x);
+          widen<T, VEC>(rr[t], gr);
+          widen<T, VEC>(ir[t], gi);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            const Gates q = gates(gr[c], gi[c], A[c] * kLog2e);
+            const float ix = q.i * x[c], ah = q.a * h[c];
+            const float root = q.s > 0.f ? q.a * q.a * rcp_fast(q.s) * ix : 0.f;
+            fa[t][c] = q.a;
+            fx[t][c] = q.s * q.i;
+            fi[t][c] = q.s * ix * (1.f - q.i);
+            fl[t][c] = (ah - root) * q.r;
+            fr[t][c] = A[c] * (1.f - q.r);
+            h[c] = __builtin_fmaf(q.s, ix, ah);
+          }
         }
-        store_vec<T, VEC>(p.dx + o, dx);
-        store_vec<T, VEC>(p.dgr + o, dgr);
-        store_vec<T, VEC>(p.dgi + o, dgi);
-      }
-    }
+#pragma unroll
+      for (int t = kCk - 1; t >= 0; --t)
+        if (FULL || t < m) {
+          const int64_t o = at + t * p.ED;
+          float dy[VEC], dx[VEC], dgr[VEC], dgi[VEC];
+          widen<T, VEC>(dr[t], dy);
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) {
+            const float g = G[c] + dy[c];
+            const float dlr = g * fl[t][c];
+            dx[c] = g * fx[t][c];
+            dgi[c] = g * fi[t][c];
+            dgr[c] = dlr * fr[t][c];
+            dA[c] += dlr;
+            G[c] = fa[t][c] * g;
+          }
+          if (w.ok) {
+            store_raw<T, VEC>(scalar(p.dx + o) + w.lo, dx);
+            store_raw<T, VEC>(scalar(p.dgr + o) + w.lo, dgr);
+            store_raw<T, VEC>(scalar(p.dgi + o) + w.lo, dgi);
+          }
+        }
+    });
   }
-  if (p.dh0 && k == 0) store_vec<float, VEC>(p.dh0 + b * p.ED + e, G);
+  if (!w.ok) return;
+  if (p.dh0 && w.k == 0) store_vec<float, VEC>(p.dh0 + w.b * p.ED + w.e0 + w.lo, G);
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) p.dA_part[(b * p.nchunks + k) * p.ED + e + c] = dA[c];
+  for (int c = 0; c < VEC; ++c) p.dA_part[w.slot(p) + c] = dA[c];
 }
 
 template <typename T, int VEC>
@@ -295,85 +592,109 @@ __global__ __launch_bounds__(256) void glr_step_kernel(const T* x, const T* gr, 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-struct GlrPlan {
+// VEC: 4 bytes a lane (256 a wave and row), or single channels where a pair
+// would straddle the row's end.
+int fwd_vec(int64_t ED, int dtype) { return dtype == SSM_BF16 && ED % 2 == 0 ? 2 : 1; }
+
+struct FwdPlan {
+  int64_t nchunks, nspans, ncg, ngroups, cw;
+  int64_t flag, sflag, map, state, bytes;  // workspace offsets
+};
+
+FwdPlan fwd_plan(int64_t Bs, int64_t L, int64_t ED, int dtype) {
+  FwdPlan f{};
+  f.cw = 64 * fwd_vec(ED, dtype);
+  f.nchunks = (L + kChunk - 1) / kChunk;
+  f.nspans = (f.nchunks + kSpan - 1) / kSpan;
+  f.ncg = (ED + f.cw - 1) / f.cw;
+  f.ngroups = Bs * f.ncg;
+  if (f.nchunks <= 1) return f;
+  const auto up = [](int64_t v) { return (v + 255) & ~int64_t(255); };
+  f.flag = 256;
+  f.sflag = f.flag + up(f.nchunks * f.ngroups * 4);
+  f.map = f.sflag + up(f.nspans * f.ngroups * 4);
+  f.state = f.map + f.nchunks * f.ngroups * f.cw * 8;
+  f.bytes = f.state + f.nspans * f.ngroups * f.cw * 4;
+  return f;
+}
+
+struct BwdPlan {
   int64_t nchunks, steps, ckrows;
 };
 
 // Chunks are whole blocks of kCk steps, as long as there are at least about
-// four waves of threads per CU (256 CUs), at most 128 steps.
-GlrPlan glr_plan(int64_t Bs, int64_t L, int64_t ED) {
-  const int64_t lanes = Bs * (ED % 4 == 0 ? ED / 4 : ED);
+// eight waves of threads per CU (256 CUs), at most 128 steps.
+BwdPlan bwd_plan(int64_t Bs, int64_t L, int64_t ED, int dtype) {
+  const int64_t cw = 64 * fwd_vec(ED, dtype), waves = Bs * ((ED + cw - 1) / cw);
   int64_t steps = 128;
-  while (steps > kCk && lanes * ((L + steps - 1) / steps) < 4 * 64 * 256) steps /= 2;
-  return GlrPlan{(L + steps - 1) / steps, steps, (L + kCk - 1) / kCk};
+  while (steps > kCk && waves * ((L + steps - 1) / steps) < 8 * 256) steps /= 2;
+  return BwdPlan{(L + steps - 1) / steps, steps, (L + kCk - 1) / kCk};
 }
 
 int glr_sizes(int64_t Bs, int64_t L, int64_t ED, int dtype, int64_t* n, int64_t* nck) {
   int64_t c, rows = L >= 0 ? (L + kCk - 1) / kCk : -1, bytes;
-  if (!mul_nn(Bs, ED, &c) || !mul_nn(c, L, n) || !mul_nn(*n, 4, &bytes)) return SSM_ERR_DIM;
-  if (!mul_nn(c, rows, nck) || !mul_nn(*nck, 16, &bytes)) return SSM_ERR_DIM;
+  if (!mul_nn(Bs, ED, &c) || !mul_nn(c, L, n) || !mul_nn(*n, 8, &bytes)) return SSM_ERR_DIM;
+  // (the backward's workspace holds 16 bytes a chunk and channel)
+  if (!mul_nn(c + 64 * Bs, rows, nck) || !mul_nn(*nck, 32, &bytes) || !mul_nn(c, rows, nck)) return SSM_ERR_DIM;
   if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
-size_t glr_agg_bytes(const GlrPlan& pl, int64_t c) { return static_cast<size_t>(pl.nchunks * c) * 8; }
-size_t glr_enter_bytes(const GlrPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 4 + 15) & ~size_t(15); }
+size_t glr_agg_bytes(const BwdPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 8 + 15) & ~size_t(15); }
+size_t glr_enter_bytes(const BwdPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 4 + 15) & ~size_t(15); }
 
 template <typename T, int VEC>
-int launch_fwd(GlrArgs<T> a, hipStream_t st) {
-  const int64_t blocks = (a.Bs * a.nchunks * a.ncg + 255) / 256;
-  if (blocks > kMaxGrid) return SSM_ERR_DIM;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (a.nchunks > 1) {
-    hipLaunchKernelGGL((glr_agg_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-    const int64_t n = a.Bs * a.ED;
-    hipLaunchKernelGGL(glr_join_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64), 0, st, a.agg, a.h0,
-                       a.enter, n, a.nchunks, a.ED, 0);
-  }
-  hipLaunchKernelGGL((glr_apply_kernel<T, VEC>), grid, dim3(256), 0, st, a);
+int launch_fwd(const GlrArgs<T>& a, const FwdPlan& f, void* ws, hipStream_t st) {
+  if (f.nchunks * f.ngroups > kMaxGrid) return SSM_ERR_DIM;
+  if (f.nchunks > 1)
+    hipLaunchKernelGGL(zero_words_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((f.map / 4 + 255) / 256, 256))),
+                       dim3(256), 0, st, static_cast<unsigned*>(ws), f.map / 4);
+  hipLaunchKernelGGL((glr_fwd_kernel<T, VEC>), dim3(static_cast<unsigned>(f.nchunks * f.ngroups)), dim3(64 * kFwdWaves),
+                     0, st, a);
   return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
 
 template <typename T, int VEC>
 int launch_bwd(GlrArgs<T> a, float* dA, hipStream_t st) {
-  const int64_t blocks = (a.Bs * a.nchunks * a.ncg + 255) / 256;
-  if (blocks > kMaxGrid) return SSM_ERR_DIM;
+  a.ncg = (a.ED + 64 * VEC - 1) / (64 * VEC), a.ngroups = a.Bs * a.ncg;
+  const int64_t blocks = (a.ngroups * a.nchunks + 3) / 4, ncol = (a.ED + 15) / 16;
+  if (a.ngroups * a.nchunks > kMaxGrid || a.Bs * ncol > kMaxGrid) return SSM_ERR_DIM;
   const dim3 grid(static_cast<unsigned>(blocks));
-  const int64_t n = a.Bs * a.ED;
   hipLaunchKernelGGL((glr_bwd_agg_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(glr_join_kernel, dim3(static_cast<unsigned>((n + 63) / 64)), dim3(64), 0, st, a.agg, a.dh_last,
-                     a.enter, n, a.nchunks, a.ED, 1);
+  hipLaunchKernelGGL(glr_join_kernel, dim3(static_cast<unsigned>(a.Bs * ncol)), dim3(256), 0, st, a.agg, a.dh_last,
+                     a.enter, a.nchunks, a.ED, ncol);
   hipLaunchKernelGGL((glr_bwd_apply_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>((a.ED + 15) / 16)), dim3(256), 0, st, a.dA_part, dA,
+  hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>(ncol)), dim3(1024), 0, st, a.dA_part, dA,
                      a.Bs * a.nchunks, a.ED);
   return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
 
 template <typename T>
 int run_fwd(const void* x, const void* gr, const void* gi, const float* A, const float* h0, void* y, float* h_last,
-            float* ckpt, int64_t Bs, int64_t L, int64_t ED, void* ws, hipStream_t st) {
-  const GlrPlan pl = glr_plan(Bs, L, ED);
+            float* ckpt, int64_t Bs, int64_t L, int64_t ED, int dtype, void* ws, hipStream_t st) {
+  const FwdPlan f = fwd_plan(Bs, L, ED, dtype);
   GlrArgs<T> a{};
   a.x = static_cast<const T*>(x), a.gr = static_cast<const T*>(gr), a.gi = static_cast<const T*>(gi);
   a.A = A, a.h0 = h0, a.y = static_cast<T*>(y), a.h_last = h_last, a.ckpt = ckpt;
-  a.Bs = Bs, a.L = L, a.ED = ED, a.nchunks = pl.nchunks, a.steps = pl.steps, a.ckrows = pl.ckrows;
-  if (pl.nchunks > 1) {
-    a.agg = static_cast<float2*>(ws);
-    a.enter = reinterpret_cast<float*>(static_cast<char*>(ws) + glr_agg_bytes(pl, Bs * ED));
+  a.Bs = Bs, a.L = L, a.ED = ED, a.ckrows = (L + kCk - 1) / kCk;
+  a.nchunks = f.nchunks, a.ngroups = f.ngroups, a.ncg = f.ncg;
+  if (f.nchunks > 1) {
+    char* w = static_cast<char*>(ws);
+    a.hdr = reinterpret_cast<unsigned*>(w), a.flag = reinterpret_cast<unsigned*>(w + f.flag);
+    a.sflag = reinterpret_cast<unsigned*>(w + f.sflag), a.map = reinterpret_cast<uint64_t*>(w + f.map);
+    a.state = reinterpret_cast<unsigned*>(w + f.state);
+    a.spin_limit = split_spin_limit();
   }
-  if (ED % 4 == 0) {
-    a.ncg = ED / 4;
-    return launch_fwd<T, 4>(a, st);
-  }
-  a.ncg = ED;
-  return launch_fwd<T, 1>(a, st);
+  if constexpr (sizeof(T) == 2)
+    if (fwd_vec(ED, dtype) == 2) return launch_fwd<T, 2>(a, f, ws, st);
+  return launch_fwd<T, 1>(a, f, ws, st);
 }
 
 template <typename T>
 int run_bwd(const void* x, const void* gr, const void* gi, const float* A, const float* ckpt, const void* dy,
             const float* dh_last, void* dx, void* dgr, void* dgi, float* dA, float* dh0, int64_t Bs, int64_t L,
-            int64_t ED, void* ws, hipStream_t st) {
-  const GlrPlan pl = glr_plan(Bs, L, ED);
+            int64_t ED, int dtype, void* ws, hipStream_t st) {
+  const BwdPlan pl = bwd_plan(Bs, L, ED, dtype);
   GlrArgs<T> a{};
   a.x = static_cast<const T*>(x), a.gr = static_cast<const T*>(gr), a.gi = static_cast<const T*>(gi);
   a.A = A, a.ckpt = const_cast<float*>(ckpt), a.dy = static_cast<const T*>(dy), a.dh_last = dh_last;
@@ -383,11 +704,8 @@ int run_bwd(const void* x, const void* gr, const void* gi, const float* A, const
   a.agg = reinterpret_cast<float2*>(w);
   a.enter = reinterpret_cast<float*>(w + glr_agg_bytes(pl, Bs * ED));
   a.dA_part = reinterpret_cast<float*>(w + glr_agg_bytes(pl, Bs * ED) + glr_enter_bytes(pl, Bs * ED));
-  if (ED % 4 == 0) {
-    a.ncg = ED / 4;
-    return launch_bwd<T, 4>(a, dA, st);
-  }
-  a.ncg = ED;
+  if constexpr (sizeof(T) == 2)
+    if (fwd_vec(ED, dtype) == 2) return launch_bwd<T, 2>(a, dA, st);
   return launch_bwd<T, 1>(a, dA, st);
 }
 
@@ -402,14 +720,13 @@ extern "C" size_t ssm_glr_ckpt_bytes(int64_t Bs, int64_t L, int64_t ED) {
 extern "C" size_t ssm_glr_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype) {
   int64_t n, nck;
   if (glr_sizes(Bs, L, ED, dtype, &n, &nck) != SSM_OK || n == 0) return 0;
-  const GlrPlan pl = glr_plan(Bs, L, ED);
-  return pl.nchunks > 1 ? glr_agg_bytes(pl, Bs * ED) + glr_enter_bytes(pl, Bs * ED) : 0;
+  return static_cast<size_t>(fwd_plan(Bs, L, ED, dtype).bytes);
 }
 
 extern "C" size_t ssm_glr_bwd_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype) {
   int64_t n, nck;
   if (glr_sizes(Bs, L, ED, dtype, &n, &nck) != SSM_OK || n == 0) return 0;
-  const GlrPlan pl = glr_plan(Bs, L, ED);
+  const BwdPlan pl = bwd_plan(Bs, L, ED, dtype);
   return glr_agg_bytes(pl, Bs * ED) + 2 * glr_enter_bytes(pl, Bs * ED);
 }
 
@@ -429,8 +746,8 @@ extern "C" int ssm_glr_fwd(const void* x, const void* gr, const void* gi, const 
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (n == 0) return fill_async(h_last, h0, cb, st) ? SSM_OK : SSM_ERR_LAUNCH;
   if (need > 0 && (!workspace || workspace_bytes < need)) return SSM_ERR_WORKSPACE;
-  return dtype == SSM_F32 ? run_fwd<float>(x, gr, gi, A, h0, y, h_last, ckpt, Bs, L, ED, workspace, st)
-                          : run_fwd<uint16_t>(x, gr, gi, A, h0, y, h_last, ckpt, Bs, L, ED, workspace, st);
+  return dtype == SSM_F32 ? run_fwd<float>(x, gr, gi, A, h0, y, h_last, ckpt, Bs, L, ED, dtype, workspace, st)
+                          : run_fwd<uint16_t>(x, gr, gi, A, h0, y, h_last, ckpt, Bs, L, ED, dtype, workspace, st);
 }
 
 extern "C" int ssm_glr_bwd(const void* x, const void* gr, const void* gi, const float* A, const float* ckpt,
@@ -454,8 +771,8 @@ extern "C" int ssm_glr_bwd(const void* x, const void* gr, const void* gi, const 
     return fill_async(dA, nullptr, ED * 4, st) && fill_async(dh0, dh_last, cb, st) ? SSM_OK : SSM_ERR_LAUNCH;
   if (!workspace || workspace_bytes < need) return SSM_ERR_WORKSPACE;
   return dtype == SSM_F32
-             ? run_bwd<float>(x, gr, gi, A, ckpt, dy, dh_last, dx, dgr, dgi, dA, dh0, Bs, L, ED, workspace, st)
-             : run_bwd<uint16_t>(x, gr, gi, A, ckpt, dy, dh_last, dx, dgr, dgi, dA, dh0, Bs, L, ED, workspace, st);
+             ? run_bwd<float>(x, gr, gi, A, ckpt, dy, dh_last, dx, dgr, dgi, dA, dh0, Bs, L, ED, dtype, workspace, st)
+             : run_bwd<uint16_t>(x, gr, gi, A, ckpt, dy, dh_last, dx, dgr, dgi, dA, dh0, Bs, L, ED, dtype, workspace, st);
 }
 
 extern "C" int ssm_glr_step(const void* x, const void* gr, const void* gi, const float* A, const float* h, void* y,
