@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // tokens of a workgroup
-constexpr int kMaxBlocks = 2048;  // workgroups of the backward (rows of partial weight gradients)
+constexpr int kMaxBlocks = 1024;  // workgroups of the backward (rows of partial weight gradients)
 
 template <typename T>
 struct RopeArgs {
@@ -217,17 +217,21 @@ __global__ __launch_bounds__(kThreads) void rope_bwd_kernel(const RopeArgs<T> p)
   }
 }
 
-// dst (D) = sum over rows of part (rows, 2, D) at offset w, in a fixed order.
-__global__ __launch_bounds__(256) void rope_dw_kernel(const float* part, float* dwq, float* dwk, int rows, int D) {
-  __shared__ float sum[16][17];
+// dwq, dwk (D) = sums over rows of part (rows, 2, D), in a fixed order: 64
+// threads of a column each sum every 64th row, their sums are added in thread
+// order.
+__global__ __launch_bounds__(1024) void rope_dw_kernel(const float* part, float* dwq, float* dwk, int rows, int D) {
+  __shared__ float sum[64][17];
   const int ce = threadIdx.x & 15, cr = threadIdx.x >> 4;
   const int e = blockIdx.x * 16 + ce;  // of 2 D
   float v = 0.f;
-  for (int r = cr; r < rows; r += 16) v += part[static_cast<int64_t>(r) * 2 * D + e];
+#pragma unroll 8
+  for (int r = cr; r < rows; r += 64) v += part[static_cast<int64_t>(r) * 2 * D + e];
   sum[cr][ce] = v;
   __syncthreads();
   if (cr != 0) return;
-  for (int j = 1; j < 16; ++j) v += sum[j][ce];
+#pragma unroll
+  for (int j = 1; j < 64; ++j) v += sum[j][ce];
   if (e < D) {
     if (dwq) dwq[e] = v;
   } else if (dwk) {
@@ -298,7 +302,7 @@ int launch_rope_bwd(RopeArgs<T> a, float* dwq, float* dwk, int64_t D, hipStream_
   else
     hipLaunchKernelGGL((rope_bwd_kernel<T, 128>), dim3(blocks), dim3(kThreads), lds, st, a);
   if (a.part)
-    hipLaunchKernelGGL(rope_dw_kernel, dim3(static_cast<unsigned>(2 * D / 16)), dim3(256), 0, st, a.part, dwq, dwk,
+    hipLaunchKernelGGL(rope_dw_kernel, dim3(static_cast<unsigned>(2 * D / 16)), dim3(1024), 0, st, a.part, dwq, dwk,
                        blocks, static_cast<int>(D));
   return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }

@@ -661,6 +661,7 @@ __global__ __launch_bounds__(256) void swa_sink_join_kernel(const SwaArgs<T> p, 
   const float* part = p.part + ((static_cast<int64_t>(b) * p.Hk + hk) * p.nblk + j / 32) * p.nchunk * 64 * D +
                       (which * 32 + j % 32) * D + d;
   float v = 0.f;
+#pragma unroll 16  // (loads in flight; the sum keeps its order)
   for (int c = 0; c < p.nchunk; ++c) v += part[static_cast<int64_t>(c) * 64 * D];
   T* dst = (which ? p.dv : p.dk) + ((static_cast<int64_t>(b) * p.Lk + j) * p.Hk + hk) * D + d;
   *dst = from_f32<T>(which ? v : v * p.scale);

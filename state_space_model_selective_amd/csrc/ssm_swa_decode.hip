@@ -13,6 +13,7 @@
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kMaxSplits = 512;
 
 template <typename T>
 struct DecodeArgs {
@@ -134,30 +135,42 @@ __global__ __launch_bounds__(64 * kWaves, 1) void swa_decode_kernel(const Decode
   }
 }
 
-// One workgroup a head: the join over the splits.
+// One workgroup a head: the join over the splits. A wave forms the splits'
+// factors, 64 at a time, then every thread sums its entry.
 template <typename T, int D>
 __global__ __launch_bounds__(D) void swa_decode_join_kernel(const DecodeArgs<T> p) {
   constexpr int R = kRecord<D>;
+  __shared__ float factor[kMaxSplits];
+  __shared__ float total;
   const int head = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq, d = threadIdx.x;
   const int hk = head / p.G, g = head % p.G;
   const float* part = p.part + (((static_cast<int64_t>(b) * p.Hk + hk) * p.GB + g / 32) * p.nsplit * 32 + g % 32) * R;
-  float m = -INFINITY;
-  for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, part[static_cast<int64_t>(s) * 32 * R + D]);
-  float sum = 0.f, val = 0.f;
-  for (int s = 0; s < p.nsplit; ++s) {
-    const float* r = part + static_cast<int64_t>(s) * 32 * R;
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r[D] - m);
-    sum = __builtin_fmaf(f, r[D + 1], sum);
-    val = __builtin_fmaf(f, r[d], val);
+  if (d < 64) {
+    float m = -INFINITY, sum = 0.f;
+    for (int s = d; s < p.nsplit; s += 64) m = fmaxf(m, part[static_cast<int64_t>(s) * 32 * R + D]);
+#pragma unroll
+    for (int x = 1; x < 64; x <<= 1) m = fmaxf(m, __shfl_xor(m, x));
+    for (int s = d; s < p.nsplit; s += 64) {
+      const float* r = part + static_cast<int64_t>(s) * 32 * R;
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(r[D] - m);
+      factor[s] = f;
+      sum = __builtin_fmaf(f, r[D + 1], sum);
+    }
+    sum = wave_sum(sum);
+    if (d == 0) total = sum;
   }
-  p.o[(static_cast<int64_t>(b) * p.Hq + head) * D + d] = from_f32<T>(sum == 0.f ? 0.f : val / sum);
+  __syncthreads();
+  float val = 0.f;
+#pragma unroll 16  // (loads in flight; the sum keeps its order)
+  for (int s = 0; s < p.nsplit; ++s) val = __builtin_fmaf(factor[s], part[static_cast<int64_t>(s) * 32 * R + d], val);
+  p.o[(static_cast<int64_t>(b) * p.Hq + head) * D + d] = from_f32<T>(total == 0.f ? 0.f : val / total);
 }
 
 // Workgroups that share a row's cache: about two for each compute unit over
 // the whole call, while each of their waves has a tile.
 int decode_splits(int64_t Bs, int64_t C, int64_t Hk, int64_t GB) {
   const int64_t want = 512 / std::max<int64_t>(1, Bs * Hk * GB);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, (C + 32 * kWaves - 1) / (32 * kWaves))));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), (C + 32 * kWaves - 1) / (32 * kWaves))));
 }
 
 int decode_sizes(int64_t Bs, int64_t C, int64_t Hq, int64_t Hk, int64_t D, double scale, int dtype, int64_t* nq,

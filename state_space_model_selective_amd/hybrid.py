@@ -12,6 +12,7 @@ its memory is not reused before the stream is done with it.
 """
 import contextlib
 import ctypes
+import functools
 
 _vp, _i64, _sz, _ci, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int, ctypes.c_double
 
@@ -45,6 +46,16 @@ class SSMStrides(ctypes.Structure):
 def _pkg():
     import state_space_model_selective_amd as ssm
     return ssm
+
+
+def _lib():
+    return _pkg().lib()
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(name, *sizes):
+    """A workspace size: it depends on the sizes alone."""
+    return int(getattr(_lib(), name)(*sizes))
 
 
 def _lead(where, name, t, ndim):
@@ -114,15 +125,18 @@ def _gpu(where, t):
 def _raw_stream(device, stream):
     import torch
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _allocating(device, stream):
     """The context in which a call's outputs and workspace are allocated."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_raw_stream(device, stream), device=device)
     return torch.cuda.stream(stream)
@@ -159,11 +173,11 @@ def ssm_glr_ckpt_shape(Bs, L, ED):
 
 
 def ssm_glr_workspace_bytes(Bs, L, ED, dtype=0):
-    return int(_pkg().lib().ssm_glr_workspace_bytes(Bs, L, ED, int(dtype)))
+    return int(_lib().ssm_glr_workspace_bytes(Bs, L, ED, int(dtype)))
 
 
 def ssm_glr_bwd_workspace_bytes(Bs, L, ED, dtype=0):
-    return int(_pkg().lib().ssm_glr_bwd_workspace_bytes(Bs, L, ED, int(dtype)))
+    return int(_lib().ssm_glr_bwd_workspace_bytes(Bs, L, ED, int(dtype)))
 
 
 def ssm_glr_fwd(x, gr, gi, A, y=None, h_last=None, ckpt=None, h0=None, workspace=None, stream=None):
@@ -184,12 +198,12 @@ def ssm_glr_fwd(x, gr, gi, A, y=None, h_last=None, ckpt=None, h0=None, workspace
     py, phl = _maybe(where, "y", y, dt, shape, dev), _maybe(where, "h_last", h_last, f32, (Bs, ED), dev)
     pck = _maybe(where, "ckpt", ckpt, f32, ssm_glr_ckpt_shape(Bs, L, ED), dev)
     _gpu(where, x)
-    L_ = _pkg().lib()
+    L_ = _lib()
     with _allocating(dev, stream):
         if y is None:
             y = torch.empty_like(x)
             py = y.data_ptr()
-        ws, pw, nw = _workspace(where, workspace, L_.ssm_glr_workspace_bytes(Bs, L, ED, code), dev)
+        ws, pw, nw = _workspace(where, workspace, _bytes("ssm_glr_workspace_bytes", Bs, L, ED, code), dev)
     _done(L_.ssm_glr_fwd(px, pr, pi, pA, ph0, py, phl, pck, Bs, L, ED, code, pw, nw, _raw_stream(dev, stream)), where)
     return y
 
@@ -217,12 +231,12 @@ def ssm_glr_bwd(x, gr, gi, A, ckpt, dy, dh_last=None, want_dh0=False, out=None, 
     pck = _dense(where, "ckpt", ckpt, f32, ssm_glr_ckpt_shape(Bs, L, ED), dev)
     pdh = _maybe(where, "dh_last", dh_last, f32, (Bs, ED), dev)
     _gpu(where, x)
-    L_ = _pkg().lib()
+    L_ = _lib()
     with _allocating(dev, stream):
         for k in ("dx", "dgr", "dgi", "dA") + (("dh0",) if want_dh0 else ()):
             if k not in o:
                 o[k] = torch.empty(kinds[k][1], dtype=kinds[k][0], device=dev)
-        ws, pw, nw = _workspace(where, workspace, L_.ssm_glr_bwd_workspace_bytes(Bs, L, ED, code), dev)
+        ws, pw, nw = _workspace(where, workspace, _bytes("ssm_glr_bwd_workspace_bytes", Bs, L, ED, code), dev)
     dh0 = o.get("dh0")
     _done(L_.ssm_glr_bwd(px, pr, pi, pA, pck, pdy, pdh, o["dx"].data_ptr(), o["dgr"].data_ptr(), o["dgi"].data_ptr(),
                          o["dA"].data_ptr(), None if dh0 is None else dh0.data_ptr(), Bs, L, ED, code, pw, nw,
@@ -250,7 +264,7 @@ def ssm_glr_step(x, gr, gi, A, h, y=None, h_out=None, stream=None):
         if h_out is None:
             h_out = torch.empty_like(h)
             pho = h_out.data_ptr()
-    _done(_pkg().lib().ssm_glr_step(px, pr, pi, pA, ph, py, pho, Bs, ED, code, _raw_stream(dev, stream)), where)
+    _done(_lib().ssm_glr_step(px, pr, pi, pA, ph, py, pho, Bs, ED, code, _raw_stream(dev, stream)), where)
     return y, h_out
 
 
@@ -302,13 +316,13 @@ def ssm_qk_rope_fwd(q, k, wq, wk, freq, pos=None, eps=1e-6, q_out=None, k_out=No
         if k_out is None:
             k_out = torch.empty((Bs, L, Hk, D), dtype=dt, device=dev)
             pko = k_out.data_ptr()
-    _done(_pkg().lib().ssm_qk_rope_fwd(*head, pp, eps, pqo, pko, Bs, L, Hq, Hk, D, R, code, _raw_stream(dev, stream)),
+    _done(_lib().ssm_qk_rope_fwd(*head, pp, eps, pqo, pko, Bs, L, Hq, Hk, D, R, code, _raw_stream(dev, stream)),
           where)
     return q_out, k_out
 
 
 def ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, dtype=0):
-    return int(_pkg().lib().ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, int(dtype)))
+    return int(_lib().ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, int(dtype)))
 
 
 def ssm_qk_rope_bwd(q, k, wq, wk, freq, dq_out, dk_out, pos=None, eps=1e-6, out=None, workspace=None, stream=None):
@@ -329,12 +343,12 @@ def ssm_qk_rope_bwd(q, k, wq, wk, freq, dq_out, dk_out, pos=None, eps=1e-6, out=
     pp = _maybe(where, "pos", pos, torch.int32, (Bs, L), dev)
     pdq, pdk = _dense(where, "dq_out", dq_out, *kinds["dq"], dev), _dense(where, "dk_out", dk_out, *kinds["dk"], dev)
     _gpu(where, q)
-    L_ = _pkg().lib()
+    L_ = _lib()
     with _allocating(dev, stream):
         for n in ("dq", "dk") + (("dwq",) if wq is not None else ()) + (("dwk",) if wk is not None else ()):
             if n not in o:
                 o[n] = torch.empty(kinds[n][1], dtype=kinds[n][0], device=dev)
-        need = L_.ssm_qk_rope_bwd_workspace_bytes(Bs, L, Hq, Hk, D, code) if "dwq" in o or "dwk" in o else 0
+        need = _bytes("ssm_qk_rope_bwd_workspace_bytes", Bs, L, Hq, Hk, D, code) if "dwq" in o or "dwk" in o else 0
         ws, pw, nw = _workspace(where, workspace, need, dev)
     dwq, dwk = o.get("dwq"), o.get("dwk")
     _done(L_.ssm_qk_rope_bwd(*head, pp, eps, pdq, pdk, o["dq"].data_ptr(), o["dk"].data_ptr(),
@@ -370,7 +384,7 @@ def ssm_qk_rope_append(q, k, v, wq, wk, freq, pos, k_cache, v_cache, sinks, eps=
         with _allocating(dev, stream):
             q_out = torch.empty((Bs, L, Hq, D), dtype=dt, device=dev)
         pqo = q_out.data_ptr()
-    _done(_pkg().lib().ssm_qk_rope_append(pq, sq, pk, sk, pv, sv, *rest, pp, eps, pqo, pkc, pvc, Bs, L, Hq, Hk, D, R,
+    _done(_lib().ssm_qk_rope_append(pq, sq, pk, sk, pv, sv, *rest, pp, eps, pqo, pkc, pvc, Bs, L, Hq, Hk, D, R,
                                           C - sinks, sinks, code, _raw_stream(dev, stream)), where)
     return q_out
 
@@ -421,12 +435,12 @@ def ssm_swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=Non
         with _allocating(dev, stream):
             o = torch.empty(q.shape, dtype=q.dtype, device=dev)
         po = o.data_ptr()
-    _done(_pkg().lib().ssm_swa_fwd(*head, po, pl, *dims, code, _raw_stream(dev, stream)), where)
+    _done(_lib().ssm_swa_fwd(*head, po, pl, *dims, code, _raw_stream(dev, stream)), where)
     return o
 
 
 def ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, sinks=0, dtype=0):
-    return int(_pkg().lib().ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, sinks, int(dtype)))
+    return int(_lib().ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, sinks, int(dtype)))
 
 
 def ssm_swa_bwd(q, k, v, o, lse, do, window, sinks=0, scale=None, lens=None, out=None, workspace=None, stream=None):
@@ -448,19 +462,19 @@ def ssm_swa_bwd(q, k, v, o, lse, do, window, sinks=0, scale=None, lens=None, out
     po, pdo = _dense(where, "o", o, dt, q.shape, dev), _dense(where, "do", do, dt, q.shape, dev)
     pl = _dense(where, "lse", lse, torch.float32, (Bs, Hq, Lq), dev)
     _gpu(where, q)
-    L_ = _pkg().lib()
+    L_ = _lib()
     with _allocating(dev, stream):
         for n in kinds:
             if n not in g:
                 g[n] = torch.empty(kinds[n][1], dtype=dt, device=dev)
-        ws, pw, nw = _workspace(where, workspace, L_.ssm_swa_bwd_workspace_bytes(Bs, Lq, Lk, Hq, Hk, D, dims[7], code), dev)
+        ws, pw, nw = _workspace(where, workspace, _bytes("ssm_swa_bwd_workspace_bytes", Bs, Lq, Lk, Hq, Hk, D, dims[7], code), dev)
     _done(L_.ssm_swa_bwd(*head, po, pl, pdo, g["dq"].data_ptr(), g["dk"].data_ptr(), g["dv"].data_ptr(), *dims, code,
                          pw, nw, _raw_stream(dev, stream)), where)
     return g
 
 
 def ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, dtype=0):
-    return int(_pkg().lib().ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, int(dtype)))
+    return int(_lib().ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, int(dtype)))
 
 
 def ssm_swa_decode(q, k_cache, v_cache, pos, scale=None, o=None, workspace=None, stream=None):
@@ -488,12 +502,12 @@ def ssm_swa_decode(q, k_cache, v_cache, pos, scale=None, o=None, workspace=None,
     pp = _dense(where, "pos", pos, torch.int32, (Bs,), dev)
     po = _maybe(where, "o", o, dt, q.shape, dev)
     _gpu(where, q)
-    L_ = _pkg().lib()
+    L_ = _lib()
     with _allocating(dev, stream):
         if o is None:
             o = torch.empty(q.shape, dtype=dt, device=dev)
             po = o.data_ptr()
-        ws, pw, nw = _workspace(where, workspace, L_.ssm_swa_decode_workspace_bytes(Bs, C, Hq, Hk, D, code), dev)
+        ws, pw, nw = _workspace(where, workspace, _bytes("ssm_swa_decode_workspace_bytes", Bs, C, Hq, Hk, D, code), dev)
     _done(L_.ssm_swa_decode(q.data_ptr(), sq, pk, pv, pp, D ** -0.5 if scale is None else float(scale), po, Bs, C, Hq,
                             Hk, D, code, pw, nw, _raw_stream(dev, stream)), where)
     return o
