@@ -233,25 +233,33 @@ __device__ __forceinline__ void add_waves(v16f (&x)[D / 32], char* lds, int wave
 
 // The tiles 0 .. n - 1 of a workgroup: load(t, buffer) starts the loads of a
 // tile, use(t, buffer) works on it. Apart, the next tile's loads are under way
-// while this one is used.
+// while this one is used; the loop goes by pairs of tiles so that the buffer is
+// a constant and LDS addresses need no arithmetic.
+template <int B>
+using Buffer = std::integral_constant<int, B>;
 template <bool SPLIT, typename L, typename U>
 __device__ __forceinline__ void over_tiles(int n, L load, U use) {
+  __syncthreads();  // nobody reads an earlier tile any more
   if constexpr (SPLIT) {
     for (int t = 0; t < n; ++t) {
-      __syncthreads();  // nobody reads the last tile any more
-      load(t, 0);
+      load(t, Buffer<0>{});
       wait_loads();
       __syncthreads();
-      use(t, 0);
+      use(t, Buffer<0>{});
+      __syncthreads();
     }
   } else {
-    __syncthreads();
-    if (n > 0) load(0, 0);
-    for (int t = 0; t < n; ++t) {
+    if (n > 0) load(0, Buffer<0>{});
+    for (int t = 0; t < n; t += 2) {
       wait_loads();
       __syncthreads();  // tile t is in LDS; nobody reads the other buffer any more
-      if (t + 1 < n) load(t + 1, (t + 1) & 1);
-      use(t, t & 1);
+      if (t + 1 < n) load(t + 1, Buffer<1>{});
+      use(t, Buffer<0>{});
+      if (t + 1 >= n) break;
+      wait_loads();
+      __syncthreads();
+      if (t + 2 < n) load(t + 2, Buffer<0>{});
+      use(t + 1, Buffer<1>{});
     }
   }
 }
@@ -290,22 +298,36 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 
   over_tiles<SPLIT>(
       tiles.n,
-      [&](int t, int buf) {
+      [&](int t, auto buf) {
         const int k0 = tiles.key0(t, KB);
         KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
         KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
       },
-      [&](int t, int buf) {
+      [&](int t, auto buf) {
         const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0, k1 = k0 + 32 * NB - 1;
         if (i0 >= p.Lq || m.none(pw0, pw1, k0, k1)) return;
         const char *ks = sm[buf][0], *vs = sm[buf][1];
         v16f s[NB];
+        {
+          Frag<T> kf[NB][KK];
 #pragma unroll
-        for (int kb = 0; kb < NB; ++kb) {
-          s[kb] = v16f{};
+          for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk) s[kb] = mma(KT::row(ks, r0 + 32 * kb + n, kk, hi), q[kk], s[kb]);
+            for (int kk = 0; kk < KK; ++kk) kf[kb][kk] = KT::row(ks, r0 + 32 * kb + n, kk, hi);
+          in_order<T>();
+#pragma unroll
+          for (int kb = 0; kb < NB; ++kb) s[kb] = v16f{};
+#pragma unroll
+          for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+            for (int kb = 0; kb < NB; ++kb) s[kb] = mma(kf[kb][kk], q[kk], s[kb]);
         }
+        Frag<T> vf[2][DB];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, r0 + 16 * h, d, lane);
+        in_order<T>();
         if (!m.all(pw0, pw1, k0, k1)) {
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb)
@@ -318,11 +340,18 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
           for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[kb][r]);
-        const float now = fmaxf(top, pair_max(mx) * sc);
-        const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - now);
-        const float ref = now == -INFINITY ? 0.f : now;  // (a row that has seen nothing: every weight is 0)
-        top = now;
-        l *= keep;
+        // the reference point moves only where a maximum passes it by 2^8: the
+        // weights then stay below 2^8, and their sums need not be scaled again
+        const float peak = pair_max(mx) * sc;
+        if (__any(peak > top + 8.f)) {
+          const float now = fmaxf(top, peak);
+          const float keep = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - now);
+          top = now;
+          l *= keep;
+#pragma unroll
+          for (int d = 0; d < DB; ++d) o[d] *= keep;
+        }
+        const float ref = top == -INFINITY ? 0.f : top;  // (a row that has seen nothing: every weight is 0)
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
@@ -331,15 +360,17 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
             l += s[kb][r];
           }
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] *= keep;
-#pragma unroll
-        for (int kb = 0; kb < NB; ++kb)
+        for (int kb = 0; kb < NB; ++kb) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const Frag<T> w8 = as_operand<T>(s[kb], h);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) o[d] = mma(KT::col(vs, r0 + 32 * kb + 16 * h, d, lane), w8, o[d]);
+            for (int d = 0; d < DB; ++d) o[d] = mma(vf[h][d], w8, o[d]);
+            if (kb + 1 < NB)
+#pragma unroll
+              for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, r0 + 32 * (kb + 1) + 16 * h, d, lane);
           }
+        }
       });
   l = pair_sum(l);
   if constexpr (SPLIT) {
@@ -417,18 +448,25 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
   v16f dq[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d) dq[d] = v16f{};
-  auto load = [&](int t, int buf) {
+  auto load = [&](int t, auto buf) {
     const int k0 = tiles.key0(t, KB);
     KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
     KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
   };
   // weights and their gradients of one block of 32 keys (rows r0 .. of the tile)
-  auto scores = [&](int buf, int r0, int k0, v16f& s, v16f& dp) {
+  auto scores = [&](auto buf, int r0, int k0, v16f& s, v16f& dp) {
+    Frag<T> kf[KK], vf[KK];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      kf[kk] = KT::row(sm[buf][0], r0 + n, kk, hi);
+      vf[kk] = KT::row(sm[buf][1], r0 + n, kk, hi);
+    }
+    if constexpr (D == 64) in_order<T>();  // (D = 128 has no registers for it)
     s = v16f{}, dp = v16f{};
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      s = mma(KT::row(sm[buf][0], r0 + n, kk, hi), q[kk], s);
-      dp = mma(KT::row(sm[buf][1], r0 + n, kk, hi), go[kk], dp);
+      s = mma(kf[kk], q[kk], s);
+      dp = mma(vf[kk], go[kk], dp);
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], sc, -lse));
@@ -443,7 +481,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
   };
   if (sizeof(T) == 2 && p.exact) {
     float sum = 0.f;
-    over_tiles<SPLIT>(tiles.n, load, [&](int t, int buf) {
+    over_tiles<SPLIT>(tiles.n, load, [&](int t, auto buf) {
       const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
       if (i0 >= p.Lq) return;
       for (int kb = 0; kb < NB; ++kb) {
@@ -464,20 +502,25 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
     delta = sum;
   }
   if (hi == 0 && i < p.Lq && (!SPLIT || wave == 0)) p.delta[st] = delta;
-  over_tiles<SPLIT>(tiles.n, load, [&](int t, int buf) {
+  over_tiles<SPLIT>(tiles.n, load, [&](int t, auto buf) {
     const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
     if (i0 >= p.Lq || m.none(pw0, pw1, k0, k0 + 32 * NB - 1)) return;
 #pragma unroll
     for (int kb = 0; kb < NB; ++kb) {
       v16f s, dp;
       scores(buf, r0 + 32 * kb, k0 + 32 * kb, s, dp);
+      Frag<T> cf[2][DB];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) cf[h][d] = KT::col(sm[buf][0], r0 + 32 * kb + 16 * h, d, lane);
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> ds = as_operand<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < DB; ++d) dq[d] = mma(KT::col(sm[buf][0], r0 + 32 * kb + 16 * h, d, lane), ds, dq[d]);
+        for (int d = 0; d < DB; ++d) dq[d] = mma(cf[h][d], ds, dq[d]);
       }
     }
   });
@@ -499,7 +542,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
 // tiles by ranges and leave float32 partial sums.
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT, bool SINK>
-__global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
+__global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
   static_assert(SPLIT || !SINK, "the sinks' workgroups share their keys");
   using Z = Shape<T, D, SPLIT>;
   constexpr int QB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
@@ -551,7 +594,7 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
 
   over_tiles<SPLIT>(
       end - first,
-      [&](int f, int buf) {
+      [&](int f, auto buf) {
         const int h = hk * p.G + (first + f) / nt, i0 = (t0 + (first + f) % nt) * QB;
         QT::template load<kNT>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[buf][0], wave, lane);
         QT::template load<kNT>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D,
@@ -563,7 +606,7 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
                            static_cast<unsigned>(i) * 4u, lds_address(&stat[buf][wave & 1][64 * part]));
         }
       },
-      [&](int f, int buf) {
+      [&](int f, auto buf) {
         const char *qs = sm[buf][0], *gs = sm[buf][1];
 #pragma unroll
         for (int rb = 0; rb < NB; ++rb) {
@@ -572,11 +615,29 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
           const int pb0 = ib + off, pb1 = pb0 + 31;
           if (ib >= p.Lq || m.none(pb0, pb1, j0, j0 + 31)) continue;
           v16f s = v16f{}, dp = v16f{};
+          {
+            Frag<T> qf[KK], gf[KK];
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk) {
-            s = mma(QT::row(qs, r0 + n, kk, hi), k[kk], s);
-            dp = mma(QT::row(gs, r0 + n, kk, hi), v[kk], dp);
+            for (int kk = 0; kk < KK; ++kk) {
+              qf[kk] = QT::row(qs, r0 + n, kk, hi);
+              gf[kk] = QT::row(gs, r0 + n, kk, hi);
+            }
+            in_order<T>();
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+              s = mma(qf[kk], k[kk], s);
+              dp = mma(gf[kk], v[kk], dp);
+            }
           }
+          Frag<T> qc[2][DB], gc[2][DB];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+              gc[h][d] = QT::col(gs, r0 + 16 * h, d, lane);
+              qc[h][d] = QT::col(qs, r0 + 16 * h, d, lane);
+            }
+          in_order<T>();
           const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq && (SINK ? j0 + 31 < p.S : j0 >= p.S);
 #pragma unroll
           for (int r4 = 0; r4 < 4; ++r4) {
@@ -604,8 +665,8 @@ __global__ __launch_bounds__(kNT, 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
             const Frag<T> wt = as_operand<T>(s, h), ds = as_operand<T>(dp, h);
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
-              dv[d] = mma(QT::col(gs, r0 + 16 * h, d, lane), wt, dv[d]);
-              dk[d] = mma(QT::col(qs, r0 + 16 * h, d, lane), ds, dk[d]);
+              dv[d] = mma(gc[h][d], wt, dv[d]);
+              dk[d] = mma(qc[h][d], ds, dk[d]);
             }
           }
         }

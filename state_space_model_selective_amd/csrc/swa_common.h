@@ -198,6 +198,16 @@ struct Tile {
   }
 };
 
+// Keeps the compiler from moving instructions across: operands are read from
+// LDS together, ahead of the products that take them, and arrive while others
+// run (left alone, each read stands right before its product, which then waits
+// for it). float32 operands take twice the registers and their products eight
+// times as long: there the compiler is left its choice.
+template <typename T>
+__device__ __forceinline__ void in_order() {
+  if constexpr (sizeof(T) == 2) __builtin_amdgcn_sched_barrier(0);
+}
+
 // Waits for the wave's outstanding loads (vmcnt(0), nothing else): the builtin,
 // which the compiler counts with, and a barrier to its reordering.
 __device__ __forceinline__ void wait_loads() {
