@@ -27,6 +27,9 @@ SOURCES = [os.path.join(_HERE, "csrc", n) for n in ("ssm_scan.hip", "ssm_scan_bw
 PROBE_LIB_PATH = os.path.join(_HERE, "libssm_valu_probe.so")
 PROBE_SOURCES = [os.path.join(_HERE, "csrc", "valu_probe.hip")]
 INCLUDE = os.path.join(_ROOT, "include")
+# direct calls for Python (host code, built against torch's headers)
+FAST_LIB_PATH = os.path.join(_HERE, "_fast_calls.so")
+FAST_SOURCE = os.path.join(_HERE, "csrc", "fast_calls.cpp")
 
 SSM_F32, SSM_BF16 = 0, 1
 # bytes of the device buffer that ssm_scan_fwd_noalloc uses in place of a workspace
@@ -84,11 +87,34 @@ def _hipcc(sources, out, verbose):
                 os.remove(o)
 
 
+def _host_extension(source, out, verbose):
+    """Compiles a Python extension against torch (host code only)."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    includes = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+                "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1",
+           "-DUSE_ROCM=1", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    cmd += [a for i in includes for a in ("-I", i)] + [source, "-o", out + ".tmp", "-L", os.path.join(home, "lib"),
+                                                       "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed:\n%s" % (cmd[0], res.stdout))
+    if verbose:
+        print(res.stdout)
+    os.replace(out + ".tmp", out)
+
+
 def build(verbose=False):
     """Compile libssm_scan.so (and the ALU issue-rate probe) for gfx950 with
-    hipcc (works without a GPU)."""
-    _hipcc(SOURCES, LIB_PATH, verbose)
-    _hipcc(PROBE_SOURCES, PROBE_LIB_PATH, verbose)
+    hipcc, and the Python extension with g++ (works without a GPU)."""
+    with concurrent.futures.ThreadPoolExecutor(3) as pool:
+        for job in [pool.submit(_hipcc, SOURCES, LIB_PATH, verbose),
+                    pool.submit(_hipcc, PROBE_SOURCES, PROBE_LIB_PATH, verbose),
+                    pool.submit(_host_extension, FAST_SOURCE, FAST_LIB_PATH, verbose)]:
+            job.result()
     global _lib, _probe
     _lib = None
     _probe = None

@@ -58,6 +58,33 @@ def _bytes(name, *sizes):
     return int(getattr(_lib(), name)(*sizes))
 
 
+class _NoFastCalls:
+    """Stands for the extension where it is not built: no call is ordinary."""
+
+    def __getattr__(self, name):
+        return lambda *a: None
+
+
+_fast = None
+
+
+def _load_fast():
+    """csrc/fast_calls.cpp: the forward and serving calls without Python's share of the time. Each returns None for a
+    call that is not an ordinary one, which then goes on below."""
+    global _fast
+    lib = _lib()
+    try:
+        from . import _fast_calls
+    except ImportError:
+        _fast = _NoFastCalls()
+        return _fast
+    for name in ("ssm_glr_step", "ssm_glr_fwd", "ssm_glr_workspace_bytes", "ssm_qk_rope_fwd", "ssm_qk_rope_append",
+                 "ssm_swa_fwd", "ssm_swa_decode", "ssm_swa_decode_workspace_bytes"):
+        _fast_calls.bind(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+    _fast = _fast_calls
+    return _fast
+
+
 def _lead(where, name, t, ndim):
     """Checks the argument that the others are checked against; its dtype code."""
     import torch
@@ -187,6 +214,9 @@ def ssm_glr_fwd(x, gr, gi, A, y=None, h_last=None, ckpt=None, h0=None, workspace
     negative. The final state goes to h_last ((Bs, ED) float32) and the states
     that ssm_glr_bwd needs to ckpt (float32, ssm_glr_ckpt_shape(Bs, L, ED)) if
     given. Returns y."""
+    r = (_fast or _load_fast()).glr_fwd(x, gr, gi, A, y, h_last, ckpt, h0, workspace, stream)
+    if r is not None:
+        return r
     import torch
     where, f32 = "ssm_glr_fwd", torch.float32
     code = _lead(where, "x", x, 3)
@@ -247,6 +277,9 @@ def ssm_glr_bwd(x, gr, gi, A, ckpt, dy, dh_last=None, want_dh0=False, out=None, 
 def ssm_glr_step(x, gr, gi, A, h, y=None, h_out=None, stream=None):
     """One token of ssm_glr_fwd: x, gr, gi (Bs, ED), the state h (Bs, ED)
     float32. Returns (y, h_out); h_out=h updates the state in place."""
+    r = (_fast or _load_fast()).glr_step(x, gr, gi, A, h, y, h_out, stream)
+    if r is not None:
+        return r
     import torch
     where, f32 = "ssm_glr_step", torch.float32
     code = _lead(where, "x", x, 2)
@@ -301,6 +334,9 @@ def ssm_qk_rope_fwd(q, k, wq, wk, freq, pos=None, eps=1e-6, q_out=None, k_out=No
     (ones); freq (R/2,) float64 radians per position, or None (no rotation);
     pos (Bs, L) int32, or None (token t at position t). Returns (q_out,
     k_out), dense."""
+    r = (_fast or _load_fast()).rope_fwd(q, k, wq, wk, freq, pos, eps, q_out, k_out, stream)
+    if r is not None:
+        return r
     import torch
     where = "ssm_qk_rope_fwd"
     (Bs, L, Hq, Hk, D, R), code, head, eps = _rope_args(where, q, k, wq, wk, freq, eps)
@@ -364,6 +400,9 @@ def ssm_qk_rope_append(q, k, v, wq, wk, freq, pos, k_cache, v_cache, sinks, eps=
     inactive). k_cache and v_cache (Bs, Hk, sinks + window, D) are written in
     place: position p < sinks in slot p, else in slot sinks + (p - sinks) %
     window."""
+    r = (_fast or _load_fast()).rope_append(q, k, v, wq, wk, freq, pos, k_cache, v_cache, sinks, eps, q_out, stream)
+    if r is not None:
+        return r
     import torch
     where = "ssm_qk_rope_append"
     (Bs, L, Hq, Hk, D, R), code, (pq, sq, pk, sk, *rest), eps = _rope_args(where, q, k, wq, wk, freq, eps)
@@ -423,6 +462,9 @@ def ssm_swa_fwd(q, k, v, window, sinks=0, scale=None, lens=None, o=None, lse=Non
     sees nothing gives zeros. Returns o (Bs, Lq, Hq, D), dense; with lse (Bs,
     Hq, Lq) float32 the log of the softmax's sum is written there, for
     ssm_swa_bwd."""
+    r = (_fast or _load_fast()).swa_fwd(q, k, v, window, sinks, scale, lens, o, lse, stream)
+    if r is not None:
+        return r
     import torch
     where = "ssm_swa_fwd"
     dims, code, head = _swa_args(where, q, k, v, window, sinks, scale, lens)
@@ -482,6 +524,9 @@ def ssm_swa_decode(q, k_cache, v_cache, pos, scale=None, o=None, workspace=None,
     keeps: q (Bs, Hq, D) (last dimension contiguous) sees the min(pos + 1, C)
     filled slots of k_cache and v_cache (Bs, Hk, C, D); pos (Bs,) int32 is the
     token's position (negative: an inactive row, zeros). Returns o (Bs, Hq, D)."""
+    r = (_fast or _load_fast()).swa_decode(q, k_cache, v_cache, pos, scale, o, workspace, stream)
+    if r is not None:
+        return r
     import torch
     where = "ssm_swa_decode"
     code = _lead(where, "q", q, 3)
