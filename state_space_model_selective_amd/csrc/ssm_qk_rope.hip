@@ -6,8 +6,9 @@
 // A head is held by D entries / 16 bytes lanes, 16 bytes each, so that every
 // access is a full 16-byte vector; the mean is a butterfly over those lanes
 // and the partner of a pair comes from another lane of the same head. A
-// workgroup takes a few tokens: it forms their angles once (64-bit reduction
-// to a fraction of a turn, then float32) in LDS, for all heads of q and k.
+// workgroup takes a few tokens and a slice of their heads: it forms the angles
+// once (64-bit reduction to a fraction of a turn, then float32) in LDS, for all
+// its heads, while its first loads are under way.
 #include "hybrid_common.h"
 
 namespace {
@@ -34,7 +35,7 @@ struct RopeArgs {
   const T* dk_out;
   float* part;
   int64_t Bs, L;
-  int Hq, Hk, half, tokens;  // half: R / 2; tokens: of a workgroup
+  int Hq, Hk, half, tokens, heads;  // half: R / 2; tokens, heads: of a workgroup
   int window, sinks;
 };
 
@@ -67,37 +68,77 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// The (token, head) pairs of a workgroup that one group of lanes takes in turn:
+// pairs g, g + G, ... of `heads` heads a token, from head h0. Tokens count from
+// the workgroup's first, which is token l0 of row b0.
+struct Walk {
+  int t, h, heads, h0, L;
+  int b, l;  // of token t
+  __device__ __forceinline__ Walk(int g, int heads_, int h0_, int b0, int l0, int L_)
+      : t(0), h(g), heads(heads_), h0(h0_), L(L_), b(b0), l(l0) {
+    wrap();
+  }
+  __device__ __forceinline__ void wrap() {
+    while (h >= heads) {
+      h -= heads;
+      ++t;
+      if (++l == L) l = 0, ++b;
+    }
+  }
+  __device__ __forceinline__ void advance(int G) {
+    h += G;
+    wrap();
+  }
+};
+
+
 template <typename T, int D, bool APPEND>
 __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs<T> p) {
-  constexpr int E = Vec16<T>::kN, LPH = D / E;
+  constexpr int E = Vec16<T>::kN, LPH = D / E, G = kThreads / LPH;
   extern __shared__ float2 cs[];
+  const unsigned L = static_cast<unsigned>(p.L);
   const int64_t first = blockIdx.x * static_cast<int64_t>(p.tokens), all = p.Bs * p.L;
   const int n = static_cast<int>(all - first < p.tokens ? all - first : p.tokens);
-  angles<T, APPEND>(p, first, n, cs);
-  __syncthreads();
-  const int li = threadIdx.x % LPH;
   const int H = p.Hq + p.Hk + (APPEND ? p.Hk : 0);
-  const int lane = threadIdx.x & 63;
+  const int h0 = blockIdx.y * p.heads, heads = H - h0 < p.heads ? H - h0 : p.heads;
+  const int64_t b0 = first / L;
+  const int li = threadIdx.x % LPH, lane = threadIdx.x & 63, j0 = li * E;
+  Walk w(threadIdx.x / LPH, heads, h0, static_cast<int>(b0), static_cast<int>(first - b0 * L), static_cast<int>(L));
+  Walk ahead = w;  // where the next load goes: two pairs ahead of the work
+  auto fetch = [&](uint4& raw) {
+    if (ahead.t < n) {
+      const int h = h0 + ahead.h;
+      const T* src = h < p.Hq ? p.q + ahead.b * p.qs.batch + ahead.l * p.qs.token + h * p.qs.head
+                     : h < p.Hq + p.Hk
+                         ? p.k + ahead.b * p.ks.batch + ahead.l * p.ks.token + (h - p.Hq) * p.ks.head
+                         : p.v + ahead.b * p.vs.batch + ahead.l * p.vs.token + (h - p.Hq - p.Hk) * p.vs.head;
+      raw = *reinterpret_cast<const uint4*>(src + j0);
+    }
+    ahead.advance(G);
+  };
+  uint4 raw, next, later;
+  fetch(raw);
+  fetch(next);
+  angles<T, APPEND>(p, first, n, cs);
   float wq[E], wk[E];
 #pragma unroll
   for (int c = 0; c < E; ++c) {
-    wq[c] = p.wq ? p.wq[li * E + c] : 1.f;
-    wk[c] = p.wk ? p.wk[li * E + c] : 1.f;
+    wq[c] = p.wq ? p.wq[j0 + c] : 1.f;
+    wk[c] = p.wk ? p.wk[j0 + c] : 1.f;
   }
+  __syncthreads();
   // where this lane's entries sit in the rotation
-  const int j0 = li * E;
   const bool turned = j0 < 2 * p.half, upper = j0 >= p.half;
   const int partner = !turned ? lane : upper ? lane - p.half / E : lane + p.half / E;
-  const int jc = upper ? j0 - p.half : j0;
-  for (int item = threadIdx.x / LPH; item < n * H; item += kThreads / LPH) {
-    const int t = item / H, h = item % H;
-    const int64_t tok = first + t, b = tok / p.L, l = tok % p.L;
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hk;
+  const int jc = turned ? (upper ? j0 - p.half : j0) : 0;
+  const float side = upper ? 1.f : -1.f;
+  while (w.t < n) {
+    const int t = w.t, h = h0 + w.h, b = w.b, l = w.l;
+    w.advance(G);
+    fetch(later);
+    const bool is_q = h < p.Hq, is_v = APPEND && h >= p.Hq + p.Hk;
     const int hh = is_q ? h : is_v ? h - p.Hq - p.Hk : h - p.Hq;
-    const T* src = is_q ? p.q + b * p.qs.batch + l * p.qs.token + hh * p.qs.head
-                 : is_v ? p.v + b * p.vs.batch + l * p.vs.token + hh * p.vs.head
-                        : p.k + b * p.ks.batch + l * p.ks.token + hh * p.ks.head;
-    const uint4 raw = *reinterpret_cast<const uint4*>(src + j0);
+    const int64_t tok = b * p.L + l;
     float x[E], o[E];
     Vec16<T>::widen(raw, x);
     float ss = 0.f;
@@ -108,35 +149,32 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs<T> p) {
     for (int c = 0; c < E; ++c) x[c] = x[c] * inv * (is_q ? wq[c] : wk[c]);
 #pragma unroll
     for (int c = 0; c < E; ++c) {
-      const float other = __shfl(x[c], partner);
+      const float other = __shfl(x[c], partner) * side;
+      o[c] = x[c];
       if (turned) {
         const float2 a = cs[t * p.half + jc + c];
-        o[c] = upper ? __builtin_fmaf(x[c], a.x, other * a.y) : __builtin_fmaf(x[c], a.x, -other * a.y);
-      } else {
-        o[c] = x[c];
+        o[c] = __builtin_fmaf(x[c], a.x, other * a.y);
       }
     }
     uint4 res = is_v ? raw : Vec16<T>::narrow(o);
     if constexpr (APPEND) {
       const int64_t p0 = p.pos[b], at = p0 + l;
-      if (p0 < 0) {
-        if (!is_q) continue;
-        res = make_uint4(0u, 0u, 0u, 0u);
-      }
       if (is_q) {
+        if (p0 < 0) res = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4*>(p.q_out + (tok * p.Hq + hh) * D + j0) = res;
-      } else {
-        const int64_t slot = at < p.sinks ? at : p.sinks + (at - p.sinks) % p.window;
-        const bool stays = at < p.sinks || p.L - 1 - l < p.window;  // no later token of this call takes the slot
+      } else if (p0 >= 0 && (at < p.sinks || p.L - 1 - l < p.window)) {
+        // (otherwise a later token of this call takes the slot)
+        const int64_t slot =
+            at < p.sinks ? at : p.sinks + static_cast<unsigned>(at - p.sinks) % static_cast<unsigned>(p.window);
         T* cache = is_v ? p.v_out : p.k_out;
-        if (stays)
-          *reinterpret_cast<uint4*>(cache + ((b * p.Hk + hh) * (static_cast<int64_t>(p.sinks) + p.window) + slot) * D +
-                                    j0) = res;
+        *reinterpret_cast<uint4*>(
+            cache + ((static_cast<int64_t>(b) * p.Hk + hh) * (static_cast<int64_t>(p.sinks) + p.window) + slot) * D + j0) = res;
       }
     } else {
       T* dst = is_q ? p.q_out + (tok * p.Hq + hh) * D : p.k_out + (tok * p.Hk + hh) * D;
       *reinterpret_cast<uint4*>(dst + j0) = res;
     }
+    raw = next, next = later;
   }
 }
 
@@ -148,58 +186,78 @@ __global__ __launch_bounds__(kThreads) void rope_bwd_kernel(const RopeArgs<T> p)
   constexpr int E = Vec16<T>::kN, LPH = D / E, G = kThreads / LPH;
   extern __shared__ float2 cs[];
   __shared__ float red[G][D];
+  const unsigned L = static_cast<unsigned>(p.L);
   const int64_t all = p.Bs * p.L;
-  const int li = threadIdx.x % LPH, H = p.Hq + p.Hk, lane = threadIdx.x & 63;
+  const int H = p.Hq + p.Hk, h0 = blockIdx.y * p.heads, heads = H - h0 < p.heads ? H - h0 : p.heads;
+  const int li = threadIdx.x % LPH, lane = threadIdx.x & 63, j0 = li * E;
   float wq[E], wk[E], dwq[E], dwk[E];
 #pragma unroll
   for (int c = 0; c < E; ++c) {
-    wq[c] = p.wq ? p.wq[li * E + c] : 1.f;
-    wk[c] = p.wk ? p.wk[li * E + c] : 1.f;
+    wq[c] = p.wq ? p.wq[j0 + c] : 1.f;
+    wk[c] = p.wk ? p.wk[j0 + c] : 1.f;
     dwq[c] = dwk[c] = 0.f;
   }
-  const int j0 = li * E;
   const bool turned = j0 < 2 * p.half, upper = j0 >= p.half;
   const int partner = !turned ? lane : upper ? lane - p.half / E : lane + p.half / E;
-  const int jc = upper ? j0 - p.half : j0;
+  const int jc = turned ? (upper ? j0 - p.half : j0) : 0;
+  const float side = upper ? -1.f : 1.f;
   for (int64_t first = blockIdx.x * static_cast<int64_t>(p.tokens); first < all;
        first += gridDim.x * static_cast<int64_t>(p.tokens)) {
     const int n = static_cast<int>(all - first < p.tokens ? all - first : p.tokens);
+    const int64_t b0 = first / L;
+    Walk w(threadIdx.x / LPH, heads, h0, static_cast<int>(b0), static_cast<int>(first - b0 * L), static_cast<int>(L));
+    int64_t o = 0, next_o = 0;
+    uint4 rx, rd, next_x, next_d;
+    auto fetch = [&](uint4& vx, uint4& vd, int64_t& at) {
+      if (w.t >= n) return;
+      const int h = h0 + w.h;
+      const bool is_q = h < p.Hq;
+      const int hh = is_q ? h : h - p.Hq;
+      const int64_t tok = w.b * p.L + w.l;
+      const T* src = is_q ? p.q + w.b * p.qs.batch + w.l * p.qs.token + hh * p.qs.head
+                          : p.k + w.b * p.ks.batch + w.l * p.ks.token + hh * p.ks.head;
+      at = (is_q ? tok * p.Hq + hh : tok * p.Hk + hh) * D + j0;
+      vx = *reinterpret_cast<const uint4*>(src + j0);
+      vd = *reinterpret_cast<const uint4*>((is_q ? p.dq_out : p.dk_out) + at);
+    };
+    fetch(rx, rd, o);
     __syncthreads();  // the last group's angles are no longer read
     angles<T, false>(p, first, n, cs);
     __syncthreads();
-    for (int item = threadIdx.x / LPH; item < n * H; item += G) {
-      const int t = item / H, h = item % H;
-      const int64_t tok = first + t, b = tok / p.L, l = tok % p.L;
-      const bool is_q = h < p.Hq;
-      const int hh = is_q ? h : h - p.Hq;
-      const T* src = is_q ? p.q + b * p.qs.batch + l * p.qs.token + hh * p.qs.head
-                          : p.k + b * p.ks.batch + l * p.ks.token + hh * p.ks.head;
-      const int64_t o = (is_q ? (tok * p.Hq + hh) : (tok * p.Hk + hh)) * D + j0;
-      float x[E], d[E];
-      Vec16<T>::widen(*reinterpret_cast<const uint4*>(src + j0), x);
-      Vec16<T>::widen(*reinterpret_cast<const uint4*>((is_q ? p.dq_out : p.dk_out) + o), d);
-      float ss = 0.f;
+    while (w.t < n) {
+      const int t = w.t;
+      const bool is_q = h0 + w.h < p.Hq;
+      w.advance(G);
+      fetch(next_x, next_d, next_o);  // under way while this pair is worked on
+      {
+        float x[E], d[E];
+        Vec16<T>::widen(rx, x);
+        Vec16<T>::widen(rd, d);
+        float ss = 0.f;
 #pragma unroll
-      for (int c = 0; c < E; ++c) ss = __builtin_fmaf(x[c], x[c], ss);
-      const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPH>(ss), 1.f / D, p.eps));
-      float m = 0.f;
+        for (int c = 0; c < E; ++c) ss = __builtin_fmaf(x[c], x[c], ss);
+        const float inv = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<LPH>(ss), 1.f / D, p.eps));
+        float m = 0.f;
 #pragma unroll
-      for (int c = 0; c < E; ++c) {
-        const float other = __shfl(d[c], partner);
-        if (turned) {
-          const float2 a = cs[t * p.half + jc + c];
-          d[c] = upper ? __builtin_fmaf(d[c], a.x, -other * a.y) : __builtin_fmaf(d[c], a.x, other * a.y);
+        for (int c = 0; c < E; ++c) {
+          const float other = __shfl(d[c], partner) * side;
+          if (turned) {
+            const float2 a = cs[t * p.half + jc + c];
+            d[c] = __builtin_fmaf(d[c], a.x, other * a.y);
+          }
+          x[c] *= inv;
+          const float g = d[c] * x[c];
+          dwq[c] += is_q ? g : 0.f;
+          dwk[c] += is_q ? 0.f : g;
+          d[c] *= is_q ? wq[c] : wk[c];
+          m = __builtin_fmaf(d[c], x[c], m);
         }
-        x[c] *= inv;
-        const float g = d[c] * x[c];
-        if (is_q) dwq[c] += g; else dwk[c] += g;
-        d[c] *= is_q ? wq[c] : wk[c];
-        m = __builtin_fmaf(d[c], x[c], m);
-      }
-      m = head_sum<LPH>(m) * (1.f / D);
+        m = head_sum<LPH>(m) * (1.f / D);
 #pragma unroll
-      for (int c = 0; c < E; ++c) d[c] = inv * __builtin_fmaf(-x[c], m, d[c]);
-      *reinterpret_cast<uint4*>((is_q ? p.q_out : p.k_out) + o) = Vec16<T>::narrow(d);
+        for (int c = 0; c < E; ++c) d[c] = inv * __builtin_fmaf(-x[c], m, d[c]);
+        *reinterpret_cast<uint4*>((is_q ? p.q_out : p.k_out) + o) = Vec16<T>::narrow(d);
+      }
+      rx = next_x, rd = next_d, o = next_o;
     }
   }
   if (!p.part) return;
@@ -212,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void rope_bwd_kernel(const RopeArgs<T> p)
     for (int j = threadIdx.x; j < D; j += kThreads) {
       float v = 0.f;
       for (int g = 0; g < G; ++g) v += red[g][j];
-      p.part[(blockIdx.x * 2ll + w) * D + j] = v;
+      p.part[((blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x) * 2 + w) * D + j] = v;
     }
   }
 }
@@ -248,24 +306,38 @@ int rope_sizes(int64_t Bs, int64_t L, int64_t Hq, int64_t Hk, int64_t D, int64_t
   if (!mul_nn(Bs, L, &t) || !mul_nn(Hq, D, nq) || !mul_nn(Hk, D, nk) || !mul_nn(t, *nq, nq) || !mul_nn(t, *nk, nk) ||
       !mul_nn(*nq, 8, &bytes) || !mul_nn(*nk, 8, &bytes) || R < 0)
     return SSM_ERR_DIM;
-  if (Hq + Hk > (1 << 20)) return SSM_ERR_DIM;
+  if (Hq + Hk > (1 << 18) || L > INT32_MAX) return SSM_ERR_DIM;
   if (dtype != SSM_F32 && dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
   if ((D != 64 && D != 128) || R > D || R % 16) return SSM_ERR_UNSUPPORTED;
   if (!(eps >= 0) || eps > 1e30) return SSM_ERR_ARG;
   return SSM_OK;
 }
 
-// Tokens of a workgroup: about eight heads' vectors a thread, at most
+// Tokens of a workgroup: about 24 vectors a thread (with eight, forming the
+// angles shows: 94 us for 2x8192 tokens of 32 + 8 heads instead of 87), at most
 // kMaxTokens (their angles fit LDS), fewer when there are few tokens.
 int rope_tokens(int64_t all, int64_t H, int64_t D, int E) {
-  int64_t t = 8 * kThreads / std::max<int64_t>(1, H * D / E);
+  int64_t t = 24 * kThreads / std::max<int64_t>(1, H * D / E);
   t = std::min<int64_t>(std::max<int64_t>(t, 1), kMaxTokens);
   while (t > 1 && all / t < 1024) t /= 2;
   return static_cast<int>(t);
 }
 
-int rope_bwd_blocks(int64_t all, int tokens) {
-  return static_cast<int>(std::min<int64_t>((all + tokens - 1) / tokens, kMaxBlocks));
+// Heads of a workgroup: all of them, or, where that would leave compute units
+// without work, slices of whole passes of its groups of lanes.
+int rope_heads(int64_t blocks, int64_t H, int64_t D, int E) {
+  const int64_t G = kThreads / (D / E), most = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, blocks));
+  const int64_t slices = std::min((H + G - 1) / G, most);
+  return static_cast<int>(((H + slices - 1) / slices + G - 1) / G * G);
+}
+
+struct RopeBwdGrid {
+  int x, y;
+};
+RopeBwdGrid rope_bwd_grid(int64_t all, int tokens, int64_t H, int64_t D, int E) {
+  const int64_t x = std::min<int64_t>((all + tokens - 1) / tokens, kMaxBlocks);
+  const int heads = rope_heads(x, H, D, E);
+  return RopeBwdGrid{static_cast<int>(x), static_cast<int>((H + heads - 1) / heads)};
 }
 
 template <typename T>
@@ -277,6 +349,7 @@ RopeArgs<T> rope_args(const void* q, ssm_strides qs, const void* k, ssm_strides 
   a.wq = wq, a.wk = wk, a.freq = freq, a.pos = pos, a.eps = static_cast<float>(eps);
   a.Bs = Bs, a.L = L, a.Hq = static_cast<int>(Hq), a.Hk = static_cast<int>(Hk), a.half = static_cast<int>(R / 2);
   a.tokens = rope_tokens(Bs * L, heads, D, Vec16<T>::kN);
+  a.heads = rope_heads((Bs * L + a.tokens - 1) / a.tokens, heads, D, Vec16<T>::kN);
   return a;
 }
 
@@ -284,7 +357,8 @@ template <typename T, bool APPEND>
 int launch_rope(const RopeArgs<T>& a, int64_t D, hipStream_t st) {
   const int64_t blocks = (a.Bs * a.L + a.tokens - 1) / a.tokens;
   if (blocks > kMaxGrid) return SSM_ERR_DIM;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  const int H = a.Hq + a.Hk + (APPEND ? a.Hk : 0);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((H + a.heads - 1) / a.heads));
   const size_t lds = static_cast<size_t>(a.tokens) * a.half * sizeof(float2);
   if (D == 64)
     hipLaunchKernelGGL((rope_kernel<T, 64, APPEND>), grid, dim3(kThreads), lds, st, a);
@@ -295,15 +369,17 @@ int launch_rope(const RopeArgs<T>& a, int64_t D, hipStream_t st) {
 
 template <typename T>
 int launch_rope_bwd(RopeArgs<T> a, float* dwq, float* dwk, int64_t D, hipStream_t st) {
-  const int blocks = rope_bwd_blocks(a.Bs * a.L, a.tokens);
+  const RopeBwdGrid g = rope_bwd_grid(a.Bs * a.L, a.tokens, a.Hq + a.Hk, D, Vec16<T>::kN);
+  a.heads = rope_heads(g.x, a.Hq + a.Hk, D, Vec16<T>::kN);
+  const dim3 grid(g.x, g.y);
   const size_t lds = static_cast<size_t>(a.tokens) * a.half * sizeof(float2);
   if (D == 64)
-    hipLaunchKernelGGL((rope_bwd_kernel<T, 64>), dim3(blocks), dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL((rope_bwd_kernel<T, 64>), grid, dim3(kThreads), lds, st, a);
   else
-    hipLaunchKernelGGL((rope_bwd_kernel<T, 128>), dim3(blocks), dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL((rope_bwd_kernel<T, 128>), grid, dim3(kThreads), lds, st, a);
   if (a.part)
     hipLaunchKernelGGL(rope_dw_kernel, dim3(static_cast<unsigned>(2 * D / 16)), dim3(1024), 0, st, a.part, dwq, dwk,
-                       blocks, static_cast<int>(D));
+                       g.x * g.y, static_cast<int>(D));
   return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
 
@@ -340,8 +416,9 @@ extern "C" size_t ssm_qk_rope_bwd_workspace_bytes(int64_t Bs, int64_t L, int64_t
                                                   int dtype) {
   int64_t nq, nk;
   if (rope_sizes(Bs, L, Hq, Hk, D, 0, 0.0, dtype, &nq, &nk) != SSM_OK || nq + nk == 0) return 0;
-  const int tokens = rope_tokens(Bs * L, Hq + Hk, D, dtype == SSM_F32 ? 4 : 8);
-  return static_cast<size_t>(rope_bwd_blocks(Bs * L, tokens)) * 2 * D * 4;
+  const int E = dtype == SSM_F32 ? 4 : 8, tokens = rope_tokens(Bs * L, Hq + Hk, D, E);
+  const RopeBwdGrid g = rope_bwd_grid(Bs * L, tokens, Hq + Hk, D, E);
+  return static_cast<size_t>(g.x) * g.y * 2 * D * 4;
 }
 
 extern "C" int ssm_qk_rope_bwd(const void* q, const ssm_strides* qs, const void* k, const ssm_strides* ks,
