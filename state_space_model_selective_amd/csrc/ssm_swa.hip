@@ -24,16 +24,21 @@ constexpr int kWaves = 4, kNT = 64 * kWaves;
 
 // Two ways for the four waves of a workgroup to share its work. Apart: each
 // owns 32 rows (queries; keys for dk and dv) and they go over the same tiles,
-// double-buffered. Together (SPLIT): all own the same 32 rows, tiles are four
-// blocks of 32, a wave takes one, and the waves' sums are added at the end --
-// four times the workgroups, for calls that would leave compute units empty.
-template <typename T, int D, bool SPLIT>
+// double-buffered. Together (SPLIT): all own the same 32 rows, each takes every
+// fourth tile of 32 rows, through LDS of its own and without barriers, and
+// their sums are added at the end -- four times the workgroups, for calls that
+// would leave compute units empty. BYTES: LDS for tiles of such a workgroup
+// (two buffers where they fit).
+template <typename T, int D, bool SPLIT, int BYTES>
 struct Shape {
   static constexpr int kOwn = SPLIT ? 32 : 32 * kWaves;  // rows of a workgroup
   // rows of an LDS tile; apart: 16 KiB of them, at most 64
-  static constexpr int kRows = SPLIT ? 32 * kWaves : 16384 / (D * static_cast<int>(sizeof(T))) < 64 ? 32 : 64;
-  static constexpr int kBufs = SPLIT ? 1 : 2;
-  static constexpr int kBlocks = SPLIT ? 1 : kRows / 32;  // blocks of a tile that a wave takes
+  static constexpr int kRows = SPLIT ? 32 : 16384 / (D * static_cast<int>(sizeof(T))) < 64 ? 32 : 64;
+  static constexpr int kSets = SPLIT ? kWaves : 1;  // of buffers
+  static constexpr int kPair = 2 * kRows * D * static_cast<int>(sizeof(T));
+  static constexpr int kBufs = SPLIT && kSets * 2 * kPair > BYTES ? 1 : 2;
+  static constexpr int kBlocks = kRows / 32;
+  static constexpr int kLoaders = SPLIT ? 64 : kNT;  // threads that load a tile
 };
 
 template <typename T>
@@ -237,29 +242,35 @@ __device__ __forceinline__ void add_waves(v16f (&x)[D / 32], char* lds, int wave
 // a constant and LDS addresses need no arithmetic.
 template <int B>
 using Buffer = std::integral_constant<int, B>;
-template <bool SPLIT, typename L, typename U>
-__device__ __forceinline__ void over_tiles(int n, L load, U use) {
+template <typename Z, bool SPLIT, typename L, typename U>
+__device__ __forceinline__ void over_tiles(int n, int wave, L load, U use) {
   __syncthreads();  // nobody reads an earlier tile any more
-  if constexpr (SPLIT) {
-    for (int t = 0; t < n; ++t) {
+  const int first = SPLIT ? wave : 0;
+  constexpr int STEP = SPLIT ? kWaves : 1;
+  if constexpr (Z::kBufs == 1) {
+    for (int t = first; t < n; t += STEP) {
+      wait_reads();
       load(t, Buffer<0>{});
       wait_loads();
-      __syncthreads();
       use(t, Buffer<0>{});
-      __syncthreads();
     }
   } else {
-    if (n > 0) load(0, Buffer<0>{});
-    for (int t = 0; t < n; t += 2) {
-      wait_loads();
-      __syncthreads();  // tile t is in LDS; nobody reads the other buffer any more
-      if (t + 1 < n) load(t + 1, Buffer<1>{});
+    auto ready = [&] {
+      wait_loads();  // the tile is in LDS
+      if constexpr (SPLIT)
+        wait_reads();
+      else
+        __syncthreads();  // nobody reads the other buffer any more
+    };
+    if (first < n) load(first, Buffer<0>{});
+    for (int t = first; t < n; t += 2 * STEP) {
+      ready();
+      if (t + STEP < n) load(t + STEP, Buffer<1>{});
       use(t, Buffer<0>{});
-      if (t + 1 >= n) break;
-      wait_loads();
-      __syncthreads();
-      if (t + 2 < n) load(t + 2, Buffer<0>{});
-      use(t + 1, Buffer<1>{});
+      if (t + STEP >= n) break;
+      ready();
+      if (t + 2 * STEP < n) load(t + 2 * STEP, Buffer<0>{});
+      use(t + STEP, Buffer<1>{});
     }
   }
 }
@@ -269,12 +280,12 @@ __device__ __forceinline__ void over_tiles(int n, L load, U use) {
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
-  using Z = Shape<T, D, SPLIT>;
+  using Z = Shape<T, D, SPLIT, 80 << 10>;  // two workgroups a compute unit
   constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
-  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][KT::kBytes];
+  __shared__ __attribute__((aligned(16))) char sm[Z::kSets][Z::kBufs][2][KT::kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 31, hi = lane >> 5;
+  const int n = lane & 31, hi = lane >> 5, set = SPLIT ? wave : 0;
   const Place<T> w = place_q(p);
   const Mask m = mask_of(p, w.b);
   const int off = p.Lk - p.Lq, ib = w.blk * Z::kOwn, i0 = SPLIT ? ib : ib + 32 * wave, i = i0 + n;
@@ -296,24 +307,24 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 #pragma unroll
   for (int d = 0; d < DB; ++d) o[d] = v16f{};
 
-  over_tiles<SPLIT>(
-      tiles.n,
+  over_tiles<Z, SPLIT>(
+      tiles.n, wave,
       [&](int t, auto buf) {
         const int k0 = tiles.key0(t, KB);
-        KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
-        KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
+        KT::template load<Z::kLoaders>(kbase, p.ks.token, k0, m.nk - 1, sm[set][buf][0], SPLIT ? 0 : wave, lane);
+        KT::template load<Z::kLoaders>(vbase, p.vs.token, k0, m.nk - 1, sm[set][buf][1], SPLIT ? 0 : wave, lane);
       },
       [&](int t, auto buf) {
-        const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0, k1 = k0 + 32 * NB - 1;
+        const int k0 = tiles.key0(t, KB), k1 = k0 + 32 * NB - 1;
         if (i0 >= p.Lq || m.none(pw0, pw1, k0, k1)) return;
-        const char *ks = sm[buf][0], *vs = sm[buf][1];
+        const char *ks = sm[set][buf][0], *vs = sm[set][buf][1];
         v16f s[NB];
         {
           Frag<T> kf[NB][KK];
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb)
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) kf[kb][kk] = KT::row(ks, r0 + 32 * kb + n, kk, hi);
+            for (int kk = 0; kk < KK; ++kk) kf[kb][kk] = KT::row(ks, 32 * kb + n, kk, hi);
           in_order<T>();
 #pragma unroll
           for (int kb = 0; kb < NB; ++kb) s[kb] = v16f{};
@@ -326,7 +337,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, r0 + 16 * h, d, lane);
+          for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, 16 * h, d, lane);
         in_order<T>();
         if (!m.all(pw0, pw1, k0, k1)) {
 #pragma unroll
@@ -368,7 +379,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
             for (int d = 0; d < DB; ++d) o[d] = mma(vf[h][d], w8, o[d]);
             if (kb + 1 < NB)
 #pragma unroll
-              for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, r0 + 32 * (kb + 1) + 16 * h, d, lane);
+              for (int d = 0; d < DB; ++d) vf[h][d] = KT::col(vs, 32 * (kb + 1) + 16 * h, d, lane);
           }
         }
       });
@@ -389,7 +400,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
     for (int d = 0; d < DB; ++d) o[d] *= f;
     top = all;
     l = sum;
-    add_waves<D>(o, sm[0][0], wave, n, hi);
+    add_waves<D>(o, &sm[0][0][0][0], wave, n, hi);
     if (wave > 0) return;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -411,12 +422,12 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
-  using Z = Shape<T, D, SPLIT>;
+  using Z = Shape<T, D, SPLIT, 80 << 10>;  // two workgroups a compute unit
   constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
-  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][KT::kBytes];
+  __shared__ __attribute__((aligned(16))) char sm[Z::kSets][Z::kBufs][2][KT::kBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 31, hi = lane >> 5;
+  const int n = lane & 31, hi = lane >> 5, set = SPLIT ? wave : 0;
   const Place<T> w = place_q(p);
   const Mask m = mask_of(p, w.b);
   const int off = p.Lk - p.Lq, ib = w.blk * Z::kOwn, i0 = SPLIT ? ib : ib + 32 * wave, i = i0 + n;
@@ -450,16 +461,16 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
   for (int d = 0; d < DB; ++d) dq[d] = v16f{};
   auto load = [&](int t, auto buf) {
     const int k0 = tiles.key0(t, KB);
-    KT::template load<kNT>(kbase, p.ks.token, k0, m.nk - 1, sm[buf][0], wave, lane);
-    KT::template load<kNT>(vbase, p.vs.token, k0, m.nk - 1, sm[buf][1], wave, lane);
+    KT::template load<Z::kLoaders>(kbase, p.ks.token, k0, m.nk - 1, sm[set][buf][0], SPLIT ? 0 : wave, lane);
+    KT::template load<Z::kLoaders>(vbase, p.vs.token, k0, m.nk - 1, sm[set][buf][1], SPLIT ? 0 : wave, lane);
   };
   // weights and their gradients of one block of 32 keys (rows r0 .. of the tile)
   auto scores = [&](auto buf, int r0, int k0, v16f& s, v16f& dp) {
     Frag<T> kf[KK], vf[KK];
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
-      kf[kk] = KT::row(sm[buf][0], r0 + n, kk, hi);
-      vf[kk] = KT::row(sm[buf][1], r0 + n, kk, hi);
+      kf[kk] = KT::row(sm[set][buf][0], r0 + n, kk, hi);
+      vf[kk] = KT::row(sm[set][buf][1], r0 + n, kk, hi);
     }
     if constexpr (D == 64) in_order<T>();  // (D = 128 has no registers for it)
     s = v16f{}, dp = v16f{};
@@ -481,13 +492,13 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
   };
   if (sizeof(T) == 2 && p.exact) {
     float sum = 0.f;
-    over_tiles<SPLIT>(tiles.n, load, [&](int t, auto buf) {
-      const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
+    over_tiles<Z, SPLIT>(tiles.n, wave, load, [&](int t, auto buf) {
+      const int k0 = tiles.key0(t, KB);
       if (i0 >= p.Lq) return;
       for (int kb = 0; kb < NB; ++kb) {
         if (m.none(pw0, pw1, k0 + 32 * kb, k0 + 32 * kb + 31)) continue;
         v16f s, dp;
-        scores(buf, r0 + 32 * kb, k0 + 32 * kb, s, dp);
+        scores(buf, 32 * kb, k0 + 32 * kb, s, dp);
 #pragma unroll
         for (int r = 0; r < 16; ++r) sum = __builtin_fmaf(s[r], dp[r], sum);
       }
@@ -502,18 +513,18 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
     delta = sum;
   }
   if (hi == 0 && i < p.Lq && (!SPLIT || wave == 0)) p.delta[st] = delta;
-  over_tiles<SPLIT>(tiles.n, load, [&](int t, auto buf) {
-    const int r0 = SPLIT ? 32 * wave : 0, k0 = tiles.key0(t, KB) + r0;
+  over_tiles<Z, SPLIT>(tiles.n, wave, load, [&](int t, auto buf) {
+    const int k0 = tiles.key0(t, KB);
     if (i0 >= p.Lq || m.none(pw0, pw1, k0, k0 + 32 * NB - 1)) return;
 #pragma unroll
     for (int kb = 0; kb < NB; ++kb) {
       v16f s, dp;
-      scores(buf, r0 + 32 * kb, k0 + 32 * kb, s, dp);
+      scores(buf, 32 * kb, k0 + 32 * kb, s, dp);
       Frag<T> cf[2][DB];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int d = 0; d < DB; ++d) cf[h][d] = KT::col(sm[buf][0], r0 + 32 * kb + 16 * h, d, lane);
+        for (int d = 0; d < DB; ++d) cf[h][d] = KT::col(sm[set][buf][0], 32 * kb + 16 * h, d, lane);
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] *= dp[r] - delta;
 #pragma unroll
@@ -525,7 +536,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
     }
   });
   if constexpr (SPLIT) {
-    add_waves<D>(dq, sm[0][0], wave, n, hi);
+    add_waves<D>(dq, &sm[0][0][0][0], wave, n, hi);
     if (wave > 0) return;
   }
   if (__ballot(!all_finite<D>(dq, p.scale))) {
@@ -544,14 +555,13 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
 template <typename T, int D, bool SPLIT, bool SINK>
 __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
   static_assert(SPLIT || !SINK, "the sinks' workgroups share their keys");
-  using Z = Shape<T, D, SPLIT>;
+  using Z = Shape<T, D, SPLIT, 150 << 10>;
   constexpr int QB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using QT = Tile<T, D, QB>;
-  constexpr int kStat = QB < 64 ? 64 : QB;
-  __shared__ __attribute__((aligned(16))) char sm[Z::kBufs][2][QT::kBytes];
-  __shared__ __attribute__((aligned(16))) float stat[Z::kBufs][2][kStat];  // lse, delta of a tile's rows
+  __shared__ __attribute__((aligned(16))) char sm[Z::kSets][Z::kBufs][2][QT::kBytes];
+  __shared__ __attribute__((aligned(16))) float stat[Z::kSets][Z::kBufs][2][64];  // lse, delta of a tile's rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n = lane & 31, hi = lane >> 5;
+  const int n = lane & 31, hi = lane >> 5, set = SPLIT ? wave : 0;
   int w = SINK ? blockIdx.x : xcd_order(blockIdx.x, p.nwork);
   int chunk = 0;
   if (SINK) {
@@ -592,25 +602,28 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
 #pragma unroll
   for (int d = 0; d < DB; ++d) dk[d] = v16f{}, dv[d] = v16f{};
 
-  over_tiles<SPLIT>(
-      end - first,
+  over_tiles<Z, SPLIT>(
+      end - first, wave,
       [&](int f, auto buf) {
         const int h = hk * p.G + (first + f) / nt, i0 = (t0 + (first + f) % nt) * QB;
-        QT::template load<kNT>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[buf][0], wave, lane);
-        QT::template load<kNT>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D, static_cast<int64_t>(p.Hq) * D,
-                               i0, p.Lq - 1, sm[buf][1], wave, lane);
-        const int part = wave >> 1;  // 64 rows of one of the two, a wave each
-        if (64 * part < kStat) {
-          const int i = i0 + 64 * part + lane < p.Lq ? i0 + 64 * part + lane : p.Lq - 1;
-          load_word_to_lds((wave & 1 ? p.delta : p.lse) + (static_cast<int64_t>(b) * p.Hq + h) * p.Lq,
-                           static_cast<unsigned>(i) * 4u, lds_address(&stat[buf][wave & 1][64 * part]));
-        }
+        const int part = SPLIT ? 0 : wave;
+        QT::template load<Z::kLoaders>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[set][buf][0],
+                                       part, lane);
+        QT::template load<Z::kLoaders>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D,
+                                       static_cast<int64_t>(p.Hq) * D, i0, p.Lq - 1, sm[set][buf][1], part, lane);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (SPLIT || wave == x) {
+            const int i = i0 + lane < p.Lq ? i0 + lane : p.Lq - 1;
+            load_word_to_lds((x ? p.delta : p.lse) + (static_cast<int64_t>(b) * p.Hq + h) * p.Lq,
+                             static_cast<unsigned>(i) * 4u, lds_address(stat[set][buf][x]));
+          }
       },
       [&](int f, auto buf) {
-        const char *qs = sm[buf][0], *gs = sm[buf][1];
+        const char *qs = sm[set][buf][0], *gs = sm[set][buf][1];
 #pragma unroll
         for (int rb = 0; rb < NB; ++rb) {
-          const int r0 = SPLIT ? 32 * wave : 32 * rb;
+          const int r0 = 32 * rb;
           const int ib = (t0 + (first + f) % nt) * QB + r0;
           const int pb0 = ib + off, pb1 = pb0 + 31;
           if (ib >= p.Lq || m.none(pb0, pb1, j0, j0 + 31)) continue;
@@ -638,11 +651,12 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
               qc[h][d] = QT::col(qs, r0 + 16 * h, d, lane);
             }
           in_order<T>();
-          const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq && (SINK ? j0 + 31 < p.S : j0 >= p.S);
+          // (keys on the other side of S are other columns: they are formed and not stored)
+          const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq;
 #pragma unroll
           for (int r4 = 0; r4 < 4; ++r4) {
-            const float4 ls = *reinterpret_cast<const float4*>(&stat[buf][0][r0 + 8 * r4 + 4 * hi]);
-            const float4 de = *reinterpret_cast<const float4*>(&stat[buf][1][r0 + 8 * r4 + 4 * hi]);
+            const float4 ls = *reinterpret_cast<const float4*>(&stat[set][buf][0][r0 + 8 * r4 + 4 * hi]);
+            const float4 de = *reinterpret_cast<const float4*>(&stat[set][buf][1][r0 + 8 * r4 + 4 * hi]);
             const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dl[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -655,7 +669,7 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
               const int i = ib + 8 * (r >> 2) + 4 * hi + (r & 3);
-              const bool seen = (i < p.Lq) & m.sees(i + off, j) & (SINK ? j < p.S : j >= p.S);
+              const bool seen = (i < p.Lq) & m.sees(i + off, j);
               s[r] = seen ? s[r] : 0.f;
               dp[r] = seen ? dp[r] : 0.f;
             }
@@ -672,8 +686,8 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
         }
       });
   if constexpr (SPLIT) {
-    add_waves<D>(dk, sm[0][0], wave, n, hi);
-    add_waves<D>(dv, sm[0][0], wave, n, hi);
+    add_waves<D>(dk, &sm[0][0][0][0], wave, n, hi);
+    add_waves<D>(dv, &sm[0][0][0][0], wave, n, hi);
     if (wave > 0) return;
   }
   const bool bad = __ballot(!all_finite<D>(dk, p.scale) || !all_finite<D>(dv, 1.f)) != 0;
@@ -777,12 +791,12 @@ SwaArgs<T> swa_args(const void* q, ssm_strides qs, const void* k, ssm_strides ks
   return a;
 }
 
-// Workgroups that share a block of 32 sinks: about two for each compute unit
-// over all blocks, at least two query tiles each.
+// Workgroups that share a block of 32 sinks: about one for each compute unit
+// over all blocks, at least eight query tiles (two a wave) each.
 int sink_chunks(int64_t Bs, int64_t Lq, int64_t Hq, int64_t Hk, int64_t blocks) {
-  const int64_t tiles = (Lq + 127) / 128 * (Hq / Hk);
-  const int64_t want = 512 / std::max<int64_t>(1, Bs * Hk * blocks);
-  return static_cast<int>(std::max<int64_t>(1, std::min(want, tiles / 2)));
+  const int64_t tiles = (Lq + 31) / 32 * (Hq / Hk);
+  const int64_t want = 256 / std::max<int64_t>(1, Bs * Hk * blocks);
+  return static_cast<int>(std::max<int64_t>(1, std::min(want, tiles / 8)));
 }
 
 // Blocks of `own` rows over heads of L rows, as p.nblk and p.nwork.

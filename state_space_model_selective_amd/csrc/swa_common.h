@@ -216,6 +216,14 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// Waits for the wave's LDS reads (lgkmcnt(0)), so that loads may overwrite what
+// they read.
+__device__ __forceinline__ void wait_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+  asm volatile("" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // arguments, mask
 // ---------------------------------------------------------------------------
