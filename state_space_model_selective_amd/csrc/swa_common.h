@@ -247,7 +247,6 @@ struct SwaArgs {
   int nblk;      // blocks of queries (or keys) of a head
   int nwork;     // workgroups
   int nchunk;    // sinks: workgroups that share a block of keys
-  int exact;     // dq: form delta from the weights in a pass of its own
   float scale;
 };
 
@@ -276,13 +275,17 @@ __device__ __forceinline__ Mask mask_of(const SwaArgs<T>& p, int b) {
   return Mask{nk, p.W, p.S};
 }
 
-// Consecutive workgroups go to the eight XCDs in turn; consecutive work (the
-// heads that share keys, neighbouring blocks of a head) should share an L2.
-// The map deals each XCD a contiguous range.
+// Consecutive workgroups go to the eight XCDs in turn; neighbouring work (the
+// heads that share keys, neighbouring blocks of a head) should share an L2. The
+// map deals the XCDs runs of kRun in turn (16384 tokens, window 2048, forward /
+// 2 x 4096, window 1024, training step: runs of 16 294 / 428 us, of 64 301 /
+// 406, a contiguous range for each XCD 298 / 409, which also leaves an XCD with
+// the short blocks at a sequence's start).
+constexpr int kRun = 64;
 __device__ __forceinline__ int xcd_order(int blk, int n) {
-  const int per = n >> 3, rest = n & 7, x = blk & 7, i = blk >> 3;
-  // XCD x gets blocks x, x + 8, ...: per of them, one more if x < rest
-  return x * per + (x < rest ? x : rest) + i;
+  const int x = blk & 7, i = blk >> 3, whole = n / (8 * kRun) * (8 * kRun);
+  if (blk >= whole) return blk;
+  return ((i / kRun) * 8 + x) * kRun + i % kRun;
 }
 
 // The key tiles (of KB keys) that positions [p0, p1] may see: those of the
