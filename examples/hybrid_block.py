@@ -1,0 +1,175 @@
+"""A hybrid block on the package's operators: a gated recurrent layer and a
+local attention layer, trained on whole sequences and then run token by token.
+
+    python examples/hybrid_block.py [--steps 20] [--tokens 32]
+
+Training wraps the forward and backward entry points in autograd functions;
+serving fills the recurrent state and the window cache from a prompt and goes
+on with the single-token calls. The two agree: main() trains on a toy task
+(predict the embedding seen a few steps before) and compares every decoded
+token with the whole sequence's forward.
+"""
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import state_space_model_selective_amd as ssm  # noqa: E402
+
+
+class GatedRecurrence(torch.autograd.Function):
+    """y = ssm_glr_fwd(x, gr, gi, A) from a zero state."""
+
+    @staticmethod
+    def forward(ctx, x, gr, gi, A):
+        ckpt = torch.empty(ssm.ssm_glr_ckpt_shape(*x.shape), dtype=torch.float32, device=x.device)
+        y = ssm.ssm_glr_fwd(x, gr, gi, A, ckpt=ckpt)
+        ctx.save_for_backward(x, gr, gi, A, ckpt)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, gr, gi, A, ckpt = ctx.saved_tensors
+        g = ssm.ssm_glr_bwd(x, gr, gi, A, ckpt, dy.contiguous())
+        return g["dx"], g["dgr"], g["dgi"], g["dA"]
+
+
+class NormRotate(torch.autograd.Function):
+    """(q, k) = ssm_qk_rope_fwd(q, k, wq, wk, freq) at positions 0, 1, ..."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, freq):
+        ctx.save_for_backward(q, k, wq, wk, freq)
+        return ssm.ssm_qk_rope_fwd(q, k, wq, wk, freq)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        g = ssm.ssm_qk_rope_bwd(*ctx.saved_tensors, dq_out.contiguous(), dk_out.contiguous())
+        return g["dq"], g["dk"], g["dwq"], g["dwk"], None
+
+
+class LocalAttention(torch.autograd.Function):
+    """o = ssm_swa_fwd(q, k, v, window, sinks)"""
+
+    @staticmethod
+    def forward(ctx, q, k, v, window, sinks):
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+        o = ssm.ssm_swa_fwd(q, k, v, window, sinks, lse=lse)
+        ctx.save_for_backward(q, k, v, o, lse)
+        ctx.span = window, sinks
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        g = ssm.ssm_swa_bwd(*ctx.saved_tensors, do.contiguous(), *ctx.span)
+        return g["dq"], g["dk"], g["dv"], None, None
+
+
+class HybridBlock(torch.nn.Module):
+    def __init__(self, width, channels, q_heads, k_heads, head_dim, window, sinks, rotated=None, device="cuda",
+                 dtype=torch.float32):
+        super().__init__()
+        self.channels, self.heads, self.head_dim = channels, (q_heads, k_heads), head_dim
+        self.window, self.sinks = window, sinks
+        kw = dict(device=device, dtype=dtype)
+        linear = lambda i, o: torch.nn.Linear(i, o, bias=False, **kw)
+        self.rec_in, self.rec_out = linear(width, 3 * channels), linear(channels, width)
+        self.att_in, self.att_out = linear(width, (q_heads + 2 * k_heads) * head_dim), linear(q_heads * head_dim, width)
+        # log decay of an open gate, -exp(rate): decays of 0.4 to 0.99
+        self.rate = torch.nn.Parameter(torch.empty(channels, device=device).uniform_(-4.6, -0.1))
+        self.wq = torch.nn.Parameter(torch.ones(head_dim, device=device))
+        self.wk = torch.nn.Parameter(torch.ones(head_dim, device=device))
+        R = head_dim if rotated is None else rotated
+        self.register_buffer("freq", 10000.0 ** (-torch.arange(0, R, 2, device=device, dtype=torch.float64) / R))
+
+    def _gates(self, x):
+        return [t.contiguous() for t in self.rec_in(x).split(self.channels, -1)]
+
+    def _heads(self, x):
+        """q, k and v as slices of the packed projection."""
+        (Hq, Hk), packed = self.heads, self.att_in(x)
+        packed = packed.view(*x.shape[:-1], Hq + 2 * Hk, self.head_dim)
+        return packed.split((Hq, Hk, Hk), -2)
+
+    def forward(self, x):
+        """A whole sequence (Bs, L, width), with gradients."""
+        x = x + self.rec_out(GatedRecurrence.apply(*self._gates(x), -self.rate.exp()))
+        q, k, v = self._heads(x)
+        q, k = NormRotate.apply(q, k, self.wq, self.wk, self.freq)
+        o = LocalAttention.apply(q, k, v, self.window, self.sinks)
+        return x + self.att_out(o.flatten(2))
+
+    def empty_state(self, Bs):
+        dev, dt, Hk, C = self.wq.device, self.att_in.weight.dtype, self.heads[1], self.sinks + self.window
+        cache = lambda: torch.empty(Bs, Hk, C, self.head_dim, device=dev, dtype=dt)
+        return {"h": torch.zeros(Bs, self.channels, device=dev), "k": cache(), "v": cache(),
+                "pos": torch.zeros(Bs, dtype=torch.int32, device=dev)}
+
+    @torch.no_grad()
+    def prefill(self, x, state):
+        """The first tokens (Bs, L, width) at once: the outputs, and the state after them."""
+        h_last = torch.empty_like(state["h"])
+        x = x + self.rec_out(ssm.ssm_glr_fwd(*self._gates(x), -self.rate.exp(), h0=state["h"], h_last=h_last))
+        q, k, v = self._heads(x)
+        ssm.ssm_qk_rope_append(q, k, v, self.wq, self.wk, self.freq, state["pos"], state["k"], state["v"], self.sinks)
+        q, k = ssm.ssm_qk_rope_fwd(q, k, self.wq, self.wk, self.freq)
+        o = ssm.ssm_swa_fwd(q, k, v, self.window, self.sinks)
+        state.update(h=h_last, pos=state["pos"] + x.shape[1])
+        return x + self.att_out(o.flatten(2))
+
+    @torch.no_grad()
+    def step(self, x, state):
+        """One token (Bs, width) of every row."""
+        y, state["h"] = ssm.ssm_glr_step(*self._gates(x), -self.rate.exp(), state["h"])
+        x = x + self.rec_out(y)
+        q, k, v = (t.unsqueeze(1) for t in self._heads(x))
+        q = ssm.ssm_qk_rope_append(q, k, v, self.wq, self.wk, self.freq, state["pos"], state["k"], state["v"], self.sinks)
+        o = ssm.ssm_swa_decode(q[:, 0], state["k"], state["v"], state["pos"])
+        state["pos"] += 1
+        return x + self.att_out(o.flatten(1))
+
+
+def train(block, steps, Bs, L, width, delay=5, seed=0):
+    """Adam on a toy task; the losses."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    opt, losses = torch.optim.Adam(block.parameters(), lr=3e-3), []
+    for _ in range(steps):
+        x = torch.randn(Bs, L, width, generator=gen, device="cuda")
+        loss = (block(x)[:, delay:] - x[:, :-delay]).square().mean()
+        opt.zero_grad()
+        loss.backward()
+        opt.step()
+        losses.append(float(loss.detach()))
+    return losses
+
+
+def decode_gap(block, Bs, prompt, tokens, width, seed=1):
+    """The largest difference between decoded tokens and the whole sequence's forward."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(Bs, prompt + tokens, width, generator=gen, device="cuda")
+    with torch.no_grad():
+        whole = block(x)
+    state = block.empty_state(Bs)
+    gap = float((block.prefill(x[:, :prompt].contiguous(), state) - whole[:, :prompt]).abs().max()) if prompt else 0.0
+    for t in range(prompt, prompt + tokens):
+        gap = max(gap, float((block.step(x[:, t].contiguous(), state) - whole[:, t]).abs().max()))
+    return gap
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--steps", type=int, default=20)
+    ap.add_argument("--tokens", type=int, default=32)
+    a = ap.parse_args()
+    torch.manual_seed(0)
+    width = 128
+    block = HybridBlock(width, channels=256, q_heads=4, k_heads=2, head_dim=64, window=24, sinks=2)
+    losses = train(block, a.steps, Bs=4, L=200, width=width)
+    print("training loss %.4f -> %.4f" % (losses[0], losses[-1]))
+    print("decoded tokens differ from the whole sequence's by at most %.2g" % decode_gap(block, 3, 40, a.tokens, width))
+
+
+if __name__ == "__main__":
+    main()

@@ -1,0 +1,116 @@
+"""The hybrid block of examples/: its gradients against 64-bit differentiation
+of the same block in elementary operations, and serving against training."""
+import importlib.util
+import math
+import os
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_block.py")
+
+
+@pytest.fixture(scope="module")
+def example():
+    spec = importlib.util.spec_from_file_location("hybrid_block", PATH)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def small(example):
+    torch.manual_seed(3)
+    return example.HybridBlock(32, channels=48, q_heads=4, k_heads=2, head_dim=64, window=10, sinks=2, rotated=32)
+
+
+def plain(block, w, x):
+    """The block on the CPU from the weights w (a dict by parameter name), in x's type."""
+    Bs, L, _ = x.shape
+    xr, gr, gi = (x @ w["rec_in.weight"].T).split(block.channels, -1)
+    a = torch.exp(-w["rate"].exp() * torch.sigmoid(gr))
+    h, hs = torch.zeros(Bs, block.channels, dtype=x.dtype), []
+    for t in range(L):
+        h = a[:, t] * h + torch.sqrt(1 - a[:, t] ** 2) * torch.sigmoid(gi[:, t]) * xr[:, t]
+        hs.append(h)
+    x = x + torch.stack(hs, 1) @ w["rec_out.weight"].T
+    Hq, Hk = block.heads
+    q, k, v = (x @ w["att_in.weight"].T).view(Bs, L, Hq + 2 * Hk, block.head_dim).split((Hq, Hk, Hk), 2)
+    freq = block.freq.cpu()
+    at = (torch.arange(L, dtype=torch.float64).unsqueeze(1) * freq).view(1, L, 1, -1)
+    R = freq.numel()
+
+    def turned(n, weight):
+        n = n / (n.square().mean(-1, keepdim=True) + 1e-6).sqrt() * weight
+        one, two = n[..., :R], n[..., R:2 * R]
+        return torch.cat([one * at.cos() - two * at.sin(), two * at.cos() + one * at.sin(), n[..., 2 * R:]], -1)
+
+    q, k = turned(q, w["wq"]), turned(k, w["wk"])
+    p, j = torch.arange(L).unsqueeze(1), torch.arange(L).unsqueeze(0)
+    seen = (j <= p) & ((p - j < block.window) | (j < block.sinks))
+    out = []
+    for h in range(Hq):
+        s = (q[:, :, h] @ k[:, :, h // (Hq // Hk)].transpose(1, 2) / math.sqrt(block.head_dim)).masked_fill(~seen, -1e300)
+        out.append(torch.softmax(s, -1) @ v[:, :, h // (Hq // Hk)])
+    return x + torch.stack(out, 2).flatten(2) @ w["att_out.weight"].T
+
+
+def test_gradients_of_the_block(example):
+    block = small(example)
+    x = torch.randn(2, 50, 32, generator=torch.Generator().manual_seed(1))
+    dy = torch.randn(2, 50, 32, generator=torch.Generator().manual_seed(2))
+    y = block(x.cuda())
+    y.backward(dy.cuda())
+    w = {n: p.detach().cpu().double().requires_grad_() for n, p in block.named_parameters()}
+    ref = plain(block, w, x.double())
+    (ref * dy.double()).sum().backward()
+    # float32 through four projections, the recurrence and the attention: some hundred roundings
+    close = lambda a, b: float((a.detach().cpu().double() - b).norm() / b.norm()) <= 200 * 2 ** -24
+    assert close(y, ref.detach())
+    for n, p in block.named_parameters():
+        assert close(p.grad, w[n].grad), n
+
+
+def test_training_lowers_the_loss(example):
+    losses = example.train(small(example), 12, Bs=4, L=60, width=32)
+    assert losses[-1] < 0.95 * losses[0], losses
+
+
+@pytest.mark.parametrize("prompt,tokens", [(0, 30), (1, 5), (7, 30), (45, 20)])
+def test_decoding_follows_the_forward(example, prompt, tokens):
+    assert example.decode_gap(small(example), 3, prompt, tokens, 32) <= 2e-5
+
+
+def test_decoding_in_a_graph(example):
+    """The step captured once and replayed: the tokens of the eager steps."""
+    block = small(example)
+    x = torch.randn(8, 3, 32, device="cuda", generator=torch.Generator("cuda").manual_seed(4))
+    eager, state = [], block.empty_state(3)
+    for t in range(8):
+        eager.append(block.step(x[t], state))
+    state, token = block.empty_state(3), torch.empty(3, 32, device="cuda")
+    h = state["h"]
+
+    def step():
+        y = block.step(token, state)
+        h.copy_(state["h"])  # the state stays where the graph reads it
+        state["h"] = h
+        return y
+
+    token.copy_(x[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step()
+    h.zero_()
+    state["pos"].zero_()
+    for t in range(8):
+        token.copy_(x[t])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager[t]), t
