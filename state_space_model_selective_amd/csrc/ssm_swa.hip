@@ -556,26 +556,34 @@ __global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
 // ---------------------------------------------------------------------------
 // dk and dv of the keys from S on, or (SINK) of those below S: every later
 // query sees these, so the workgroups of a block of 32 sinks share the query
-// tiles by ranges and leave float32 partial sums.
+// tiles by ranges and leave float32 partial sums. Both are one launch, the
+// sinks' workgroups the last: they fill the compute units of the workgroups of
+// the last keys, which few queries see.
 // ---------------------------------------------------------------------------
+template <typename T, int D, bool SPLIT>
+using KeyShape = Shape<T, D, SPLIT, 150 << 10>;
+template <typename Z, int BYTES>  // LDS of a workgroup's tiles
+constexpr int kTileBytes = Z::kSets * Z::kBufs * 2 * BYTES;
+
 template <typename T, int D, bool SPLIT, bool SINK>
-__global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
+__device__ __forceinline__ void dkdv_block(const SwaArgs<T>& p, int w, char* lds, float (*lds_stat)[2][64]) {
   static_assert(SPLIT || !SINK, "the sinks' workgroups share their keys");
-  using Z = Shape<T, D, SPLIT, 150 << 10>;
+  using Z = KeyShape<T, D, SPLIT>;
   constexpr int QB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using QT = Tile<T, D, QB>;
-  __shared__ __attribute__((aligned(16))) char sm[Z::kSets][Z::kBufs][2][QT::kBytes];
-  __shared__ __attribute__((aligned(16))) float stat[Z::kSets][Z::kBufs][2][64];  // lse, delta of a tile's rows
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 31, hi = lane >> 5, set = SPLIT ? wave : 0;
-  int w = SINK ? blockIdx.x : xcd_order(blockIdx.x, p.nwork);
+  auto sm = [&](int buf, int x) { return lds + ((set * Z::kBufs + buf) * 2 + x) * QT::kBytes; };  // q (0), do (1)
+  auto stat = [&](int buf, int x) { return lds_stat[set * Z::kBufs + buf][x]; };  // lse, delta of a tile's rows
+  float* part = SINK ? p.part + static_cast<int64_t>(w) * 64 * D : nullptr;        // dk, dv of 32 keys
+  const int nblk = SINK ? p.sblk : p.nblk;
   int chunk = 0;
   if (SINK) {
     chunk = w % p.nchunk;
     w /= p.nchunk;
   }
-  const int blk = w % p.nblk;
-  w /= p.nblk;
+  const int blk = w % nblk;
+  w /= nblk;
   const int hk = w % p.Hk, b = w / p.Hk;
   const Mask m = mask_of(p, b);
   const int off = p.Lk - p.Lq, jb = blk * Z::kOwn, jend = jb + Z::kOwn - 1;
@@ -612,21 +620,21 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
       end - first, wave,
       [&](int f, auto buf) {
         const int h = hk * p.G + (first + f) / nt, i0 = (t0 + (first + f) % nt) * QB;
-        const int part = SPLIT ? 0 : wave;
-        QT::template load<Z::kLoaders>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm[set][buf][0],
-                                       part, lane);
+        const int share = SPLIT ? 0 : wave;
+        QT::template load<Z::kLoaders>(p.q + b * p.qs.batch + h * p.qs.head, p.qs.token, i0, p.Lq - 1, sm(buf, 0),
+                                       share, lane);
         QT::template load<Z::kLoaders>(p.dout + (static_cast<int64_t>(b) * p.Lq * p.Hq + h) * D,
-                                       static_cast<int64_t>(p.Hq) * D, i0, p.Lq - 1, sm[set][buf][1], part, lane);
+                                       static_cast<int64_t>(p.Hq) * D, i0, p.Lq - 1, sm(buf, 1), share, lane);
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (SPLIT || wave == x) {
             const int i = i0 + lane < p.Lq ? i0 + lane : p.Lq - 1;
             load_word_to_lds((x ? p.delta : p.lse) + (static_cast<int64_t>(b) * p.Hq + h) * p.Lq,
-                             static_cast<unsigned>(i) * 4u, lds_address(stat[set][buf][x]));
+                             static_cast<unsigned>(i) * 4u, lds_address(stat(buf, x)));
           }
       },
       [&](int f, auto buf) {
-        const char *qs = sm[set][buf][0], *gs = sm[set][buf][1];
+        const char *qs = sm(buf, 0), *gs = sm(buf, 1);
 #pragma unroll
         for (int rb = 0; rb < NB; ++rb) {
           const int r0 = 32 * rb;
@@ -661,8 +669,8 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
           const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq;
 #pragma unroll
           for (int r4 = 0; r4 < 4; ++r4) {
-            const float4 ls = *reinterpret_cast<const float4*>(&stat[set][buf][0][r0 + 8 * r4 + 4 * hi]);
-            const float4 de = *reinterpret_cast<const float4*>(&stat[set][buf][1][r0 + 8 * r4 + 4 * hi]);
+            const float4 ls = *reinterpret_cast<const float4*>(stat(buf, 0) + r0 + 8 * r4 + 4 * hi);
+            const float4 de = *reinterpret_cast<const float4*>(stat(buf, 1) + r0 + 8 * r4 + 4 * hi);
             const float lv[4] = {ls.x, ls.y, ls.z, ls.w}, dl[4] = {de.x, de.y, de.z, de.w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -692,8 +700,8 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
         }
       });
   if constexpr (SPLIT) {
-    add_waves<D>(dk, &sm[0][0][0][0], wave, n, hi);
-    add_waves<D>(dv, &sm[0][0][0][0], wave, n, hi);
+    add_waves<D>(dk, lds, wave, n, hi);
+    add_waves<D>(dv, lds, wave, n, hi);
     if (wave > 0) return;
   }
   const bool bad = __ballot(!all_finite<D>(dk, p.scale) || !all_finite<D>(dv, 1.f)) != 0;
@@ -708,7 +716,6 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
       store_col<T, D>(p.dv + o, dv, 1.f, hi);
     }
   } else {
-    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 64 * D;  // dk, dv of 32 keys
     if (!bad) {
       store_col<float, D>(part + n * D, dk, 1.f, hi);
       store_col<float, D>(part + (32 + n) * D, dv, 1.f, hi);
@@ -730,6 +737,20 @@ __global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dk
   }
 }
 
+template <typename T, int D, bool SPLIT>
+__global__ __launch_bounds__(kNT, D == 64 && sizeof(T) == 2 ? 2 : 1) void swa_dkdv_kernel(const SwaArgs<T> p) {
+  using Z = KeyShape<T, D, SPLIT>;
+  using ZS = KeyShape<T, D, true>;
+  constexpr int own = kTileBytes<Z, Tile<T, D, Z::kRows>::kBytes>, sink = kTileBytes<ZS, Tile<T, D, ZS::kRows>::kBytes>;
+  __shared__ __attribute__((aligned(16))) char sm[own > sink ? own : sink];
+  __shared__ __attribute__((aligned(16))) float stat[ZS::kSets * ZS::kBufs > 2 ? ZS::kSets * ZS::kBufs : 2][2][64];
+  const int w = blockIdx.x;
+  if (w < p.nwork)
+    dkdv_block<T, D, SPLIT, false>(p, xcd_order(w, p.nwork), sm, stat);
+  else
+    dkdv_block<T, D, true, true>(p, w - p.nwork, sm, stat);
+}
+
 // dk and dv of the sinks: the sum of the partial sums, in order.
 template <typename T>
 __global__ __launch_bounds__(256) void swa_sink_join_kernel(const SwaArgs<T> p, int Bs, int D) {
@@ -739,7 +760,7 @@ __global__ __launch_bounds__(256) void swa_sink_join_kernel(const SwaArgs<T> p, 
   const int d = static_cast<int>(item % D), which = static_cast<int>(item / D % 2);
   const int64_t row = item / D / 2;
   const int hk = static_cast<int>(row % p.Hk), j = static_cast<int>(row / p.Hk % keys), b = static_cast<int>(row / p.Hk / keys);
-  const float* part = p.part + ((static_cast<int64_t>(b) * p.Hk + hk) * p.nblk + j / 32) * p.nchunk * 64 * D +
+  const float* part = p.part + ((static_cast<int64_t>(b) * p.Hk + hk) * p.sblk + j / 32) * p.nchunk * 64 * D +
                       (which * 32 + j % 32) * D + d;
   float v = 0.f;
 #pragma unroll 16  // (loads in flight; the sum keeps its order)
@@ -770,9 +791,9 @@ int swa_sizes(int64_t Bs, int64_t Lq, int64_t Lk, int64_t Hq, int64_t Hk, int64_
   if (D != 64 && D != 128) return SSM_ERR_UNSUPPORTED;
   if (!(scale > 0) || scale > 1e30) return SSM_ERR_ARG;
   z->es = dtype == SSM_F32 ? 4 : 2;
-  // workgroups of the largest launch
+  // workgroups of the largest launch (dk and dv: those of the keys and of the sinks)
   int64_t w;
-  if (!mul_nn(Bs * Hq, (std::max(Lq, Lk) + 31) / 32, &w) || w > kMaxGrid) return SSM_ERR_DIM;
+  if (!mul_nn(Bs * Hq, (std::max(Lq, Lk) + 31) / 32, &w) || w > kMaxGrid / 2) return SSM_ERR_DIM;
   return SSM_OK;
 }
 
@@ -908,20 +929,17 @@ extern "C" int ssm_swa_bwd(const void* q, const ssm_strides* qs, const void* k, 
       set_blocks(&a, Bs, Hq, Lq, 128);
       hipLaunchKernelGGL((swa_dq_kernel<T, DD, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
     }
-    if (sinks < Lk) {
-      if (together(Bs, Hk, Lk)) {
-        set_blocks(&a, Bs, Hk, Lk, 32);
-        hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
-      } else {
-        set_blocks(&a, Bs, Hk, Lk, 128);
-        hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, false, false>), dim3(a.nwork), dim3(kNT), 0, st, a);
-      }
-    }
+    a.nwork = 0;
+    const bool apart = sinks < Lk && !together(Bs, Hk, Lk);
+    if (sinks < Lk) set_blocks(&a, Bs, Hk, Lk, apart ? 128 : 32);
+    const int64_t nb = sink_blocks(sinks, Lk);
+    a.sblk = static_cast<int>(nb), a.nchunk = sink_chunks(Bs, Lq, Hq, Hk, nb);
+    const dim3 grid(static_cast<unsigned>(a.nwork + Bs * Hk * nb * a.nchunk));
+    if (apart)
+      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, false>), grid, dim3(kNT), 0, st, a);
+    else
+      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true>), grid, dim3(kNT), 0, st, a);
     if (sinks > 0) {
-      const int64_t nb = sink_blocks(sinks, Lk);
-      a.nblk = static_cast<int>(nb), a.nchunk = sink_chunks(Bs, Lq, Hq, Hk, nb);
-      a.nwork = static_cast<int>(Bs * Hk * nb * a.nchunk);
-      hipLaunchKernelGGL((swa_dkdv_kernel<T, DD, true, true>), dim3(a.nwork), dim3(kNT), 0, st, a);
       const int64_t items = Bs * std::min(sinks, Lk) * Hk * 2 * D;
       hipLaunchKernelGGL((swa_sink_join_kernel<T>), dim3(static_cast<unsigned>((items + 255) / 256)), dim3(256), 0, st,
                          a, static_cast<int>(Bs), static_cast<int>(D));

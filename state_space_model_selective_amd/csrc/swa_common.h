@@ -245,7 +245,8 @@ struct SwaArgs {
   float* part;   // sinks: partial dk and dv
   int Lq, Lk, Hq, Hk, G, W, S;
   int nblk;      // blocks of queries (or keys) of a head
-  int nwork;     // workgroups
+  int sblk;      // blocks of sinks of a head
+  int nwork;     // workgroups (without the sinks')
   int nchunk;    // sinks: workgroups that share a block of keys
   float scale;
 };
