@@ -41,6 +41,12 @@ struct Shape {
   static constexpr int kLoaders = SPLIT ? 64 : kNT;  // threads that load a tile
 };
 
+// Workgroups of fwd and dq a compute unit. The operands of float32 at D = 128
+// spill at two (2 x 4096 x 16/4 heads, window 512: forward 537 us, 410 at one);
+// the other forms fit, and two hide each other's waits.
+template <typename T, int D>
+constexpr int kSpread = D == 128 && sizeof(T) == 4 ? 1 : 2;
+
 template <typename T>
 struct Place {
   int b, hk, h, blk;
@@ -280,7 +286,7 @@ __device__ __forceinline__ void over_tiles(int n, int wave, L load, U use) {
 // forward
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
+__global__ __launch_bounds__(kNT, (kSpread<T, D>)) void swa_fwd_kernel(const SwaArgs<T> p) {
   using Z = Shape<T, D, SPLIT, 80 << 10>;  // two workgroups a compute unit
   constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
@@ -427,7 +433,7 @@ __global__ __launch_bounds__(kNT, 2) void swa_fwd_kernel(const SwaArgs<T> p) {
 // ---------------------------------------------------------------------------
 constexpr int kExactKeys = 256;
 template <typename T, int D, bool SPLIT>
-__global__ __launch_bounds__(kNT, 2) void swa_dq_kernel(const SwaArgs<T> p) {
+__global__ __launch_bounds__(kNT, (kSpread<T, D>)) void swa_dq_kernel(const SwaArgs<T> p) {
   using Z = Shape<T, D, SPLIT, 80 << 10>;  // two workgroups a compute unit
   constexpr int KB = Z::kRows, NB = Z::kBlocks, KK = D / 16, DB = D / 32;
   using KT = Tile<T, D, KB>;
