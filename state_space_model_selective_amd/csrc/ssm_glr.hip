@@ -8,9 +8,8 @@
 // step's part of it in registers, its workgroup joins eight of them to a chunk
 // of 128 steps, and chunks pass maps and states on through the workspace (see
 // Handoff); then every step's state follows from the one entering the wave.
-// Backward: the maps of the adjoint, chunk by chunk, their fold along the
-// sequence, then every chunk again from its entering adjoint, in blocks of 16
-// steps whose states start from the forward's checkpoints.
+// Backward: the same against time with the maps of the adjoint, states starting
+// from the forward's checkpoints every 16 steps.
 #include <type_traits>
 
 #include "hybrid_common.h"
@@ -143,7 +142,7 @@ struct GlrArgs {
   T* dgi;
   float* dh0;
   int64_t Bs, L, ED, ckrows;
-  // forward: the hand-off
+  // the hand-off
   unsigned* hdr;        // tickets, 64 bytes apart
   unsigned* flag;       // [chunk][group]: the chunk's map is there
   uint64_t* state;      // [span][group][channel]: the state entering the span, and 1 once it is there
@@ -151,16 +150,14 @@ struct GlrArgs {
   int64_t nchunks, ngroups, ncg;  // ncg: groups of 64 VEC channels of a row; ngroups = Bs ncg
   unsigned spin_limit;
   // backward
-  float2* agg;     // (Bs, nchunks, ED): (P, H) of each chunk
-  float* enter;    // (Bs, nchunks, ED): the adjoint entering each chunk
   float* dA_part;  // (Bs, nchunks, ED)
-  int64_t steps;
 };
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-// Handoff between the chunks of a channel group. Chunks are dealt out by
+// Handoff between the chunks of a channel group, in time order (forward) or
+// against it (backward). Chunks are dealt out by
 // tickets, from eight queues that hold an eighth of the groups each, chunk k of
 // all of them before any chunk k + 1; a workgroup takes from the queue of its
 // XCD first. So whatever a chunk waits for has been taken by a workgroup that
@@ -180,7 +177,8 @@ struct GlrArgs {
 // Waits are bounded: if one ever gives up, the chunk takes NaN as its entering
 // state.
 constexpr int kSpan = 16;
-constexpr int kFwdWaves = 8, kChunk = kFwdWaves * kCk;
+constexpr int kFwdWaves = 8;  // of a chunk
+constexpr int bwd_waves(int vec) { return vec == 1 ? 8 : 4; }
 
 __device__ __forceinline__ void publish_fence() {
   asm volatile("" ::: "memory");
@@ -213,17 +211,6 @@ __device__ __forceinline__ void run_steps(int m, F body) {
     body(std::integral_constant<bool, false>{});
 }
 
-// Chunk, group, batch row and channel group of a work item. (A division runs on
-// the vector unit; the results go back to scalars so that addresses do too.)
-template <typename T>
-__device__ __forceinline__ void locate(const GlrArgs<T>& p, unsigned item, int64_t* k, int64_t* group, int64_t* b,
-                                       int64_t* cg) {
-  const unsigned ng = static_cast<unsigned>(p.ngroups), nc = static_cast<unsigned>(p.ncg);
-  const unsigned kk = __builtin_amdgcn_readfirstlane(item / ng), g = item - kk * ng;
-  const unsigned bb = __builtin_amdgcn_readfirstlane(g / nc);
-  *k = kk, *group = g, *b = bb, *cg = g - bb * nc;
-}
-
 constexpr int kQueues = 8, kTicketWords = 16;
 // Chunk and group of the next ticket; (-1, -1) if every queue is empty.
 template <typename T>
@@ -241,6 +228,70 @@ __device__ __forceinline__ void take_chunk(const GlrArgs<T>& p, int (&out)[2]) {
     if (j < n * static_cast<unsigned>(p.nchunks)) {
       out[0] = static_cast<int>(j / n), out[1] = static_cast<int>(g0 + j % n);
       return;
+    }
+  }
+}
+
+// Chunk k (in the order of the tickets) with the map (cp, ch): h, on entry the
+// state entering the first chunk, becomes the one entering this chunk. For one
+// wave of the workgroup.
+template <typename T, int VEC>
+__device__ __forceinline__ void hand_on(const GlrArgs<T>& p, int64_t k, int64_t group, int lane, const float (&cp)[VEC],
+                                        const float (&ch)[VEC], float (&h)[VEC]) {
+  const int64_t span = k / kSpan, cw = 64 * VEC, mine = lane * VEC;
+  const int place = static_cast<int>(k % kSpan);
+  const bool more = k + 1 < p.nchunks;
+  if (more && place < kSpan - 1) {
+    uint64_t* to = p.map + (k * p.ngroups + group) * cw + mine;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c)
+      __hip_atomic_store(to + c, __builtin_bit_cast(uint64_t, make_float2(cp[c], ch[c])), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    publish_fence();
+    if (lane == 0) put_flag(p.flag + k * p.ngroups + group);
+  }
+  // the maps before this chunk in its span, joined
+  unsigned* flag = p.flag + (span * kSpan + lane) * p.ngroups + group;
+  bool good = wait_for(
+      [&] { return lane >= place || __hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0; },
+      p.spin_limit);
+  float bp[VEC], bh[VEC];
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) bp[c] = 1.f, bh[c] = 0.f;
+#pragma unroll 5
+  for (int j = 0; j < place; ++j) {
+    uint64_t* from = p.map + ((span * kSpan + j) * p.ngroups + group) * cw + mine;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const float2 v = __builtin_bit_cast(float2, __hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+      bp[c] *= v.x;
+      bh[c] = __builtin_fmaf(v.x, bh[c], v.y);
+    }
+  }
+  if (span > 0) {
+    uint64_t* from = p.state + (span * p.ngroups + group) * cw + mine;
+    good = wait_for(
+               [&] {
+                 bool all = true;
+#pragma unroll
+                 for (int c = 0; c < VEC; ++c) {
+                   const uint64_t v = __hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                   h[c] = __uint_as_float(static_cast<unsigned>(v));
+                   all = all && (v >> 32) != 0;
+                 }
+                 return all;
+               },
+               p.spin_limit) &&
+           good;
+  }
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) h[c] = good ? __builtin_fmaf(bp[c], h[c], bh[c]) : __builtin_nanf("");
+  if (more && place == kSpan - 1) {
+    uint64_t* to = p.state + ((span + 1) * p.ngroups + group) * cw + mine;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const uint64_t v = __float_as_uint(__builtin_fmaf(cp[c], h[c], ch[c]));
+      __hip_atomic_store(to + c, v | (uint64_t(1) << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
 }
@@ -267,7 +318,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void glr_fwd_kernel(const GlrArg
   const int64_t e = cg * 64 * VEC + lane * VEC;
   const bool ok = e < p.ED;  // (ED is a multiple of VEC)
   const unsigned lo = ok ? lane * VEC : 0;  // the lane's channel after the group's first
-  const int64_t t0 = k * kChunk + wave * kCk, left = p.L - t0;
+  const int64_t t0 = k * kFwdWaves * kCk + wave * kCk, left = p.L - t0;
   const int m = left < 0 ? 0 : left < kCk ? static_cast<int>(left) : kCk;  // steps of this wave
   const int64_t at = (b * p.L + t0) * p.ED + cg * 64 * VEC;
 
@@ -319,64 +370,7 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void glr_fwd_kernel(const GlrArg
       }
       h[c] = p.h0 && ok ? p.h0[b * p.ED + e + c] : 0.f;
     }
-    if (p.nchunks > 1) {
-      const int64_t span = k / kSpan, cw = 64 * VEC, mine = lane * VEC;
-      const int place = static_cast<int>(k % kSpan);
-      const bool more = k + 1 < p.nchunks;
-      if (more && place < kSpan - 1) {
-        uint64_t* to = p.map + (k * p.ngroups + group) * cw + mine;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c)
-          __hip_atomic_store(to + c, __builtin_bit_cast(uint64_t, make_float2(cp[c], ch[c])), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-        publish_fence();
-        if (lane == 0) put_flag(p.flag + k * p.ngroups + group);
-      }
-      // the maps before this chunk in its span, joined
-      unsigned* flag = p.flag + (span * kSpan + lane) * p.ngroups + group;
-      bool good = wait_for(
-          [&] { return lane >= place || __hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0; },
-          p.spin_limit);
-      float bp[VEC], bh[VEC];
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) bp[c] = 1.f, bh[c] = 0.f;
-#pragma unroll 5
-      for (int j = 0; j < place; ++j) {
-        uint64_t* from = p.map + ((span * kSpan + j) * p.ngroups + group) * cw + mine;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const float2 v = __builtin_bit_cast(float2, __hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-          bp[c] *= v.x;
-          bh[c] = __builtin_fmaf(v.x, bh[c], v.y);
-        }
-      }
-      if (span > 0) {
-        uint64_t* from = p.state + (span * p.ngroups + group) * cw + mine;
-        good = wait_for(
-                   [&] {
-                     bool all = true;
-#pragma unroll
-                     for (int c = 0; c < VEC; ++c) {
-                       const uint64_t v = __hip_atomic_load(from + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                       h[c] = __uint_as_float(static_cast<unsigned>(v));
-                       all = all && (v >> 32) != 0;
-                     }
-                     return all;
-                   },
-                   p.spin_limit) &&
-               good;
-      }
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) h[c] = good ? __builtin_fmaf(bp[c], h[c], bh[c]) : __builtin_nanf("");
-      if (more && place == kSpan - 1) {
-        uint64_t* to = p.state + ((span + 1) * p.ngroups + group) * cw + mine;
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          const uint64_t v = __float_as_uint(__builtin_fmaf(cp[c], h[c], ch[c]));
-          __hip_atomic_store(to + c, v | (uint64_t(1) << 32), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        }
-      }
-    }
+    if (p.nchunks > 1) hand_on<T, VEC>(p, k, group, lane, cp, ch, h);
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
       entering[lane][c] = h[c];
@@ -413,187 +407,169 @@ __global__ __launch_bounds__(64 * kFwdWaves, 4) void glr_fwd_kernel(const GlrArg
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// enter[k] = the adjoint entering chunk k from the chunks after it and `init`.
-// 16 channels a workgroup; a channel's chunks are shared by 16 threads, which
-// join the maps of a run each, then walk their run from its entering adjoint.
-__global__ __launch_bounds__(256) void glr_join_kernel(const float2* agg, const float* init, float* enter,
-                                                       int64_t nchunks, int64_t ED, int64_t ncol) {
-  __shared__ float2 runs[16][16];
-  const int ce = threadIdx.x & 15, seg = threadIdx.x >> 4;
-  const int64_t b = blockIdx.x / ncol, e = (blockIdx.x % ncol) * 16 + ce;
-  const bool ok = e < ED;
-  // run `seg` of the reversed order: chunks hi - 1 down to lo
-  const int64_t hi = nchunks - nchunks * seg / 16, lo = nchunks - nchunks * (seg + 1) / 16;
-  const int64_t at = b * nchunks * ED + e;
-  float P = 1.f, H = 0.f;
-  if (ok)
-#pragma unroll 8
-    for (int64_t k = hi - 1; k >= lo; --k) {
-      const float2 m = agg[at + k * ED];
-      P *= m.x;
-      H = __builtin_fmaf(m.x, H, m.y);
-    }
-  runs[seg][ce] = make_float2(P, H);
+// One pass as well: a wave takes a block of 16 steps, whose states start from
+// the forward's checkpoint. It forms the gates once and keeps what the way back
+// needs of a step in registers: a and the factors of g in dx, dgi, dla r and
+// dgr. The adjoint's map of the block, G -> P G + H with G entering after its
+// last step and leaving before its first (a_t applied), is joined and handed on
+// like the forward's, from the last chunk to the first. Two workgroups share a
+// compute unit: eight waves of 122 registers each, or, with channel pairs (216
+// registers), four.
+//   4x8192x5120 bf16: 501 us for 2.39 GB (4.8 TB/s, a copy's rate); a pass over
+// gr and dy for the maps ahead of it instead of the hand-off: 590 us. The
+// vector unit is close behind the memory. Forward and backward there: 797 us;
+// 850 in chunks of 128 steps, 875 in chunks of 32, 965 with single channels.
+// 8x1024x1536 float32: 121 us, 127 in chunks of 64 steps.
+template <typename T, int VEC>
+__global__ __launch_bounds__(64 * bwd_waves(VEC), VEC == 1 ? 4 : 2) void glr_bwd_kernel(const GlrArgs<T> p) {
+  constexpr int WAVES = bwd_waves(VEC);
+  __shared__ float2 maps[WAVES][64][VEC];
+  __shared__ float entering[64][VEC], sums[WAVES][64][VEC];
+  __shared__ int s_taken[2];
+  using Raw = typename RawOf<T, VEC>::type;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t order = 0, group = blockIdx.x;
+  if (p.nchunks > 1) {
+    if (threadIdx.x == 0) take_chunk(p, s_taken);
+    __syncthreads();
+    order = __builtin_amdgcn_readfirstlane(s_taken[0]);
+    group = __builtin_amdgcn_readfirstlane(s_taken[1]);
+    if (order < 0) return;  // (cannot happen: as many workgroups as chunks)
+  }
+  const int64_t k = p.nchunks - 1 - order;
+  const int64_t b = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(group) / static_cast<unsigned>(p.ncg));
+  const int64_t cg = group - b * p.ncg;
+  const int64_t e = cg * 64 * VEC + lane * VEC;
+  const bool ok = e < p.ED;  // (ED is a multiple of VEC)
+  const unsigned lo = ok ? lane * VEC : 0;  // the lane's channel after the group's first
+  const int64_t t0 = k * WAVES * kCk + wave * kCk, left = p.L - t0;
+  const int m = left < 0 ? 0 : left < kCk ? static_cast<int>(left) : kCk;  // steps of this wave
+  const int64_t at = (b * p.L + t0) * p.ED + cg * 64 * VEC;
+
+  float P[VEC], H[VEC], A[VEC];
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) P[c] = 1.f, H[c] = 0.f, A[c] = p.A[cg * 64 * VEC + lo + c];
+  float fa[kCk][VEC], fx[kCk][VEC], fi[kCk][VEC], fl[kCk][VEC], fr[kCk][VEC];
+  Raw dr[kCk];
+  if (m > 0) run_steps(m, [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    Raw xr[kCk], rr[kCk], ir[kCk];
+    float h[VEC];
+    load_vec<float, VEC>(p.ckpt + (b * p.ckrows + t0 / kCk) * p.ED + cg * 64 * VEC + lo, h);
+#pragma unroll
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) {
+        xr[t] = load_raw<T, VEC>(scalar(p.x + at + t * p.ED) + lo);
+        rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + lo);
+        ir[t] = load_raw<T, VEC>(scalar(p.gi + at + t * p.ED) + lo);
+      }
+#pragma unroll
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) dr[t] = load_raw<T, VEC>(scalar(p.dy + at + t * p.ED) + lo);
+#pragma unroll
+    for (int t = 0; t < kCk; ++t)
+      if (FULL || t < m) {
+        float x[VEC], gr[VEC], gi[VEC];
+        widen<T, VEC>(xr[t], x);
+        widen<T, VEC>(rr[t], gr);
+        widen<T, VEC>(ir[t], gi);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const Gates q = gates(gr[c], gi[c], A[c] * kLog2e);
+          const float ix = q.i * x[c], ah = q.a * h[c];
+          const float root = q.s > 0.f ? q.a * q.a * rcp_fast(q.s) * ix : 0.f;
+          fa[t][c] = q.a;
+          fx[t][c] = q.s * q.i;
+          fi[t][c] = q.s * ix * (1.f - q.i);
+          fl[t][c] = (ah - root) * q.r;
+          fr[t][c] = A[c] * (1.f - q.r);
+          h[c] = __builtin_fmaf(q.s, ix, ah);
+        }
+      }
+#pragma unroll
+    for (int t = kCk - 1; t >= 0; --t)
+      if (FULL || t < m) {
+        float dy[VEC];
+        widen<T, VEC>(dr[t], dy);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          P[c] *= fa[t][c];
+          H[c] = fa[t][c] * (H[c] + dy[c]);
+        }
+      }
+  });
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) maps[wave][lane][c] = make_float2(P[c], H[c]);
   __syncthreads();
-  if (!ok) return;
-  float g = init ? init[b * ED + e] : 0.f;
-  for (int s = 0; s < seg; ++s) g = __builtin_fmaf(runs[s][ce].x, g, runs[s][ce].y);
-#pragma unroll 8
-  for (int64_t k = hi - 1; k >= lo; --k) {
-    const float2 m = agg[at + k * ED];
-    enter[at + k * ED] = g;
-    g = __builtin_fmaf(m.x, g, m.y);
+  if (wave == 0) {
+    float g[VEC], cp[VEC], ch[VEC];  // (cp, ch): the chunk's map
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      cp[c] = 1.f, ch[c] = 0.f;
+#pragma unroll
+      for (int w = WAVES - 1; w >= 0; --w) {
+        const float2 v = maps[w][lane][c];
+        cp[c] *= v.x;
+        ch[c] = __builtin_fmaf(v.x, ch[c], v.y);
+      }
+      g[c] = p.dh_last && ok ? p.dh_last[b * p.ED + e + c] : 0.f;
+    }
+    if (p.nchunks > 1) hand_on<T, VEC>(p, order, group, lane, cp, ch, g);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      entering[lane][c] = g[c];
+      if (p.dh0 && ok && k == 0) p.dh0[b * p.ED + e + c] = __builtin_fmaf(cp[c], g[c], ch[c]);
+    }
   }
-}
-
-// A wave's chunk and its group of 64 VEC channels; false past the end.
-template <typename T, int VEC>
-struct BwdPlace {
-  int64_t b, k, e0, t0, n;  // first channel, first step, steps
-  unsigned lo;              // the lane's channel after e0
-  bool ok;
-  __device__ __forceinline__ bool find(const GlrArgs<T>& p) {
-    const int lane = threadIdx.x & 63;
-    const unsigned item = blockIdx.x * 4u + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (item >= p.ngroups * p.nchunks) return false;
-    int64_t group, cg;
-    locate(p, item, &k, &group, &b, &cg);
-    e0 = cg * 64 * VEC;
-    ok = e0 + lane * VEC < p.ED;
-    lo = ok ? lane * VEC : 0;
-    t0 = k * p.steps;
-    n = p.L - t0 < p.steps ? p.L - t0 : p.steps;
-    return true;
-  }
-  // of an array (Bs, nchunks, ED)
-  __device__ __forceinline__ int64_t slot(const GlrArgs<T>& p) const { return (b * p.nchunks + k) * p.ED + e0 + lo; }
-};
-
-// The adjoint's aggregate of a chunk: G -> P G + H with G entering after the
-// chunk's last step and leaving before its first (a_t applied).
-template <typename T, int VEC>
-__global__ __launch_bounds__(256) void glr_bwd_agg_kernel(const GlrArgs<T> p) {
-  using Raw = typename RawOf<T, VEC>::type;
-  BwdPlace<T, VEC> w;
-  if (!w.find(p)) return;
-  float A2[VEC], P[VEC], H[VEC];
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) A2[c] = p.A[w.e0 + w.lo + c] * kLog2e, P[c] = 1.f, H[c] = 0.f;
-  for (int64_t blk = (w.n + kCk - 1) / kCk - 1; blk >= 0; --blk) {
-    const int m = static_cast<int>(w.n - blk * kCk < kCk ? w.n - blk * kCk : kCk);
-    const int64_t at = (w.b * p.L + w.t0 + blk * kCk) * p.ED + w.e0;
-    run_steps(m, [&](auto full) {
-      constexpr bool FULL = decltype(full)::value;
-      Raw rr[kCk], dr[kCk];
-#pragma unroll
-      for (int t = kCk - 1; t >= 0; --t)
-        if (FULL || t < m) {
-          rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + w.lo);
-          dr[t] = load_raw<T, VEC>(scalar(p.dy + at + t * p.ED) + w.lo);
-        }
-#pragma unroll
-      for (int t = kCk - 1; t >= 0; --t)
-        if (FULL || t < m) {
-          float gr[VEC], dy[VEC];
-          widen<T, VEC>(rr[t], gr);
-          widen<T, VEC>(dr[t], dy);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            const float a = __builtin_amdgcn_exp2f(A2[c] * sigmoid_fast(gr[c]));
-            P[c] *= a;
-            H[c] = a * (H[c] + dy[c]);
-          }
-        }
-    });
-  }
-  if (w.ok)
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) p.agg[w.slot(p) + c] = make_float2(P[c], H[c]);
-}
-
-// Blocks of kCk steps in reverse order. A block's gates are formed once, going
-// forwards from its checkpoint; what the way back needs of a step stays in
-// registers: a and the factors of g in dx, dgi, dla r and dgr.
-template <typename T, int VEC>
-__global__ __launch_bounds__(256, 2) void glr_bwd_apply_kernel(const GlrArgs<T> p) {
-  using Raw = typename RawOf<T, VEC>::type;
-  BwdPlace<T, VEC> w;
-  if (!w.find(p)) return;
-  float A[VEC], G[VEC], dA[VEC];
+  __syncthreads();
+  float G[VEC], dA[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) {
-    A[c] = p.A[w.e0 + w.lo + c];
     dA[c] = 0.f;
-    G[c] = p.enter[w.slot(p) + c];
+    G[c] = entering[lane][c];
+#pragma unroll
+    for (int w = WAVES - 1; w > 0; --w)
+      if (w > wave) {
+        const float2 v = maps[w][lane][c];
+        G[c] = __builtin_fmaf(v.x, G[c], v.y);
+      }
   }
-  for (int64_t blk = (w.n + kCk - 1) / kCk - 1; blk >= 0; --blk) {
-    const int64_t tb = w.t0 + blk * kCk;
-    const int m = static_cast<int>(w.n - blk * kCk < kCk ? w.n - blk * kCk : kCk);
-    const int64_t at = (w.b * p.L + tb) * p.ED + w.e0;
-    run_steps(m, [&](auto full) {
-      constexpr bool FULL = decltype(full)::value;
-      Raw xr[kCk], rr[kCk], ir[kCk], dr[kCk];
-      float h[VEC];
-      load_vec<float, VEC>(p.ckpt + (w.b * p.ckrows + tb / kCk) * p.ED + w.e0 + w.lo, h);
+  if (m > 0) run_steps(m, [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
 #pragma unroll
-      for (int t = 0; t < kCk; ++t)
-        if (FULL || t < m) {
-          xr[t] = load_raw<T, VEC>(scalar(p.x + at + t * p.ED) + w.lo);
-          rr[t] = load_raw<T, VEC>(scalar(p.gr + at + t * p.ED) + w.lo);
-          ir[t] = load_raw<T, VEC>(scalar(p.gi + at + t * p.ED) + w.lo);
+    for (int t = kCk - 1; t >= 0; --t)
+      if (FULL || t < m) {
+        const int64_t o = at + t * p.ED;
+        float dy[VEC], dx[VEC], dgr[VEC], dgi[VEC];
+        widen<T, VEC>(dr[t], dy);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const float g = G[c] + dy[c];
+          const float dlr = g * fl[t][c];
+          dx[c] = g * fx[t][c];
+          dgi[c] = g * fi[t][c];
+          dgr[c] = dlr * fr[t][c];
+          dA[c] += dlr;
+          G[c] = fa[t][c] * g;
         }
-#pragma unroll
-      for (int t = kCk - 1; t >= 0; --t)
-        if (FULL || t < m) dr[t] = load_raw<T, VEC>(scalar(p.dy + at + t * p.ED) + w.lo);
-      float fa[kCk][VEC], fx[kCk][VEC], fi[kCk][VEC], fl[kCk][VEC], fr[kCk][VEC];
-#pragma unroll
-      for (int t = 0; t < kCk; ++t)
-        if (FULL || t < m) {
-          float x[VEC], gr[VEC], gi[VEC];
-          widen<T, VEC>(xr[t], x);
-          widen<T, VEC>(rr[t], gr);
-          widen<T, VEC>(ir[t], gi);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            const Gates q = gates(gr[c], gi[c], A[c] * kLog2e);
-            const float ix = q.i * x[c], ah = q.a * h[c];
-            const float root = q.s > 0.f ? q.a * q.a * rcp_fast(q.s) * ix : 0.f;
-            fa[t][c] = q.a;
-            fx[t][c] = q.s * q.i;
-            fi[t][c] = q.s * ix * (1.f - q.i);
-            fl[t][c] = (ah - root) * q.r;
-            fr[t][c] = A[c] * (1.f - q.r);
-            h[c] = __builtin_fmaf(q.s, ix, ah);
-          }
+        if (ok) {
+          store_raw<T, VEC>(scalar(p.dx + o) + lo, dx);
+          store_raw<T, VEC>(scalar(p.dgr + o) + lo, dgr);
+          store_raw<T, VEC>(scalar(p.dgi + o) + lo, dgi);
         }
+      }
+  });
 #pragma unroll
-      for (int t = kCk - 1; t >= 0; --t)
-        if (FULL || t < m) {
-          const int64_t o = at + t * p.ED;
-          float dy[VEC], dx[VEC], dgr[VEC], dgi[VEC];
-          widen<T, VEC>(dr[t], dy);
+  for (int c = 0; c < VEC; ++c) sums[wave][lane][c] = dA[c];
+  __syncthreads();
+  if (wave == 0 && ok)
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            const float g = G[c] + dy[c];
-            const float dlr = g * fl[t][c];
-            dx[c] = g * fx[t][c];
-            dgi[c] = g * fi[t][c];
-            dgr[c] = dlr * fr[t][c];
-            dA[c] += dlr;
-            G[c] = fa[t][c] * g;
-          }
-          if (w.ok) {
-            store_raw<T, VEC>(scalar(p.dx + o) + w.lo, dx);
-            store_raw<T, VEC>(scalar(p.dgr + o) + w.lo, dgr);
-            store_raw<T, VEC>(scalar(p.dgi + o) + w.lo, dgi);
-          }
-        }
-    });
-  }
-  if (!w.ok) return;
-  if (p.dh0 && w.k == 0) store_vec<float, VEC>(p.dh0 + w.b * p.ED + w.e0 + w.lo, G);
+    for (int c = 0; c < VEC; ++c) {
+      float v = 0.f;
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) p.dA_part[w.slot(p) + c] = dA[c];
+      for (int w = 0; w < WAVES; ++w) v += sums[w][lane][c];
+      p.dA_part[(b * p.nchunks + k) * p.ED + e + c] = v;
+    }
 }
 
 template <typename T, int VEC>
@@ -622,17 +598,17 @@ __global__ __launch_bounds__(256) void glr_step_kernel(const T* x, const T* gr, 
 // ---------------------------------------------------------------------------
 // VEC: 4 bytes a lane (256 a wave and row), or single channels where a pair
 // would straddle the row's end.
-int fwd_vec(int64_t ED, int dtype) { return dtype == SSM_BF16 && ED % 2 == 0 ? 2 : 1; }
+int vec_of(int64_t ED, int dtype) { return dtype == SSM_BF16 && ED % 2 == 0 ? 2 : 1; }
 
-struct FwdPlan {
+struct Plan {
   int64_t nchunks, nspans, ncg, ngroups, cw;
   int64_t flag, state, map, bytes;  // workspace offsets; what lies before `map` starts as zero
 };
 
-FwdPlan fwd_plan(int64_t Bs, int64_t L, int64_t ED, int dtype) {
-  FwdPlan f{};
-  f.cw = 64 * fwd_vec(ED, dtype);
-  f.nchunks = (L + kChunk - 1) / kChunk;
+Plan plan(int64_t Bs, int64_t L, int64_t ED, int vec, int waves) {
+  Plan f{};
+  f.cw = 64 * vec;
+  f.nchunks = (L + waves * kCk - 1) / (waves * kCk);
   f.nspans = (f.nchunks + kSpan - 1) / kSpan;
   f.ncg = (ED + f.cw - 1) / f.cw;
   f.ngroups = Bs * f.ncg;
@@ -645,19 +621,6 @@ FwdPlan fwd_plan(int64_t Bs, int64_t L, int64_t ED, int dtype) {
   return f;
 }
 
-struct BwdPlan {
-  int64_t nchunks, steps, ckrows;
-};
-
-// Chunks are whole blocks of kCk steps, as long as there are at least about
-// eight waves of threads per CU (256 CUs), at most 128 steps.
-BwdPlan bwd_plan(int64_t Bs, int64_t L, int64_t ED, int dtype) {
-  const int64_t cw = 64 * fwd_vec(ED, dtype), waves = Bs * ((ED + cw - 1) / cw);
-  int64_t steps = 128;
-  while (steps > kCk && waves * ((L + steps - 1) / steps) < 8 * 256) steps /= 2;
-  return BwdPlan{(L + steps - 1) / steps, steps, (L + kCk - 1) / kCk};
-}
-
 int glr_sizes(int64_t Bs, int64_t L, int64_t ED, int dtype, int64_t* n, int64_t* nck) {
   int64_t c, rows = L >= 0 ? (L + kCk - 1) / kCk : -1, bytes;
   if (!mul_nn(Bs, ED, &c) || !mul_nn(c, L, n) || !mul_nn(*n, 8, &bytes)) return SSM_ERR_DIM;
@@ -667,42 +630,13 @@ int glr_sizes(int64_t Bs, int64_t L, int64_t ED, int dtype, int64_t* n, int64_t*
   return SSM_OK;
 }
 
-size_t glr_agg_bytes(const BwdPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 8 + 15) & ~size_t(15); }
-size_t glr_enter_bytes(const BwdPlan& pl, int64_t c) { return (static_cast<size_t>(pl.nchunks * c) * 4 + 15) & ~size_t(15); }
-
-template <typename T, int VEC>
-int launch_fwd(const GlrArgs<T>& a, const FwdPlan& f, void* ws, hipStream_t st) {
-  if (f.nchunks * f.ngroups > kMaxGrid) return SSM_ERR_DIM;
-  if (f.nchunks > 1)
-    hipLaunchKernelGGL(zero_words_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((f.map / 4 + 255) / 256, 1024))),
-                       dim3(256), 0, st, static_cast<unsigned*>(ws), f.map / 4);
-  hipLaunchKernelGGL((glr_fwd_kernel<T, VEC>), dim3(static_cast<unsigned>(f.nchunks * f.ngroups)), dim3(64 * kFwdWaves),
-                     0, st, a);
-  return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
-}
-
-template <typename T, int VEC>
-int launch_bwd(GlrArgs<T> a, float* dA, hipStream_t st) {
-  a.ncg = (a.ED + 64 * VEC - 1) / (64 * VEC), a.ngroups = a.Bs * a.ncg;
-  const int64_t blocks = (a.ngroups * a.nchunks + 3) / 4, ncol = (a.ED + 15) / 16;
-  if (a.ngroups * a.nchunks > kMaxGrid || a.Bs * ncol > kMaxGrid) return SSM_ERR_DIM;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  hipLaunchKernelGGL((glr_bwd_agg_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(glr_join_kernel, dim3(static_cast<unsigned>(a.Bs * ncol)), dim3(256), 0, st, a.agg, a.dh_last,
-                     a.enter, a.nchunks, a.ED, ncol);
-  hipLaunchKernelGGL((glr_bwd_apply_kernel<T, VEC>), grid, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>(ncol)), dim3(1024), 0, st, a.dA_part, dA,
-                     a.Bs * a.nchunks, a.ED);
-  return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
-}
-
+// The arguments that both directions share, the hand-off's in the workspace,
+// which is cleared where it has to be.
 template <typename T>
-int run_fwd(const void* x, const void* gr, const void* gi, const float* A, const float* h0, void* y, float* h_last,
-            float* ckpt, int64_t Bs, int64_t L, int64_t ED, int dtype, void* ws, hipStream_t st) {
-  const FwdPlan f = fwd_plan(Bs, L, ED, dtype);
+GlrArgs<T> glr_args(const void* x, const void* gr, const void* gi, const float* A, int64_t Bs, int64_t L, int64_t ED,
+                    const Plan& f, void* ws, hipStream_t st) {
   GlrArgs<T> a{};
-  a.x = static_cast<const T*>(x), a.gr = static_cast<const T*>(gr), a.gi = static_cast<const T*>(gi);
-  a.A = A, a.h0 = h0, a.y = static_cast<T*>(y), a.h_last = h_last, a.ckpt = ckpt;
+  a.x = static_cast<const T*>(x), a.gr = static_cast<const T*>(gr), a.gi = static_cast<const T*>(gi), a.A = A;
   a.Bs = Bs, a.L = L, a.ED = ED, a.ckrows = (L + kCk - 1) / kCk;
   a.nchunks = f.nchunks, a.ngroups = f.ngroups, a.ncg = f.ncg;
   if (f.nchunks > 1) {
@@ -710,29 +644,53 @@ int run_fwd(const void* x, const void* gr, const void* gi, const float* A, const
     a.hdr = reinterpret_cast<unsigned*>(w), a.flag = reinterpret_cast<unsigned*>(w + f.flag);
     a.state = reinterpret_cast<uint64_t*>(w + f.state), a.map = reinterpret_cast<uint64_t*>(w + f.map);
     a.spin_limit = split_spin_limit();
+    hipLaunchKernelGGL(zero_words_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((f.map / 4 + 255) / 256, 1024))),
+                       dim3(256), 0, st, static_cast<unsigned*>(ws), f.map / 4);
   }
+  return a;
+}
+
+template <typename T>
+int run_fwd(const void* x, const void* gr, const void* gi, const float* A, const float* h0, void* y, float* h_last,
+            float* ckpt, int64_t Bs, int64_t L, int64_t ED, int dtype, void* ws, hipStream_t st) {
+  const int vec = vec_of(ED, dtype);
+  const Plan f = plan(Bs, L, ED, vec, kFwdWaves);
+  if (f.nchunks * f.ngroups > kMaxGrid) return SSM_ERR_DIM;
+  GlrArgs<T> a = glr_args<T>(x, gr, gi, A, Bs, L, ED, f, ws, st);
+  a.h0 = h0, a.y = static_cast<T*>(y), a.h_last = h_last, a.ckpt = ckpt;
+  const dim3 grid(static_cast<unsigned>(f.nchunks * f.ngroups)), block(64 * kFwdWaves);
   if constexpr (sizeof(T) == 2)
-    if (fwd_vec(ED, dtype) == 2) return launch_fwd<T, 2>(a, f, ws, st);
-  return launch_fwd<T, 1>(a, f, ws, st);
+    if (vec == 2) {
+      hipLaunchKernelGGL((glr_fwd_kernel<T, 2>), grid, block, 0, st, a);
+      return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
+    }
+  hipLaunchKernelGGL((glr_fwd_kernel<T, 1>), grid, block, 0, st, a);
+  return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
 
 template <typename T>
 int run_bwd(const void* x, const void* gr, const void* gi, const float* A, const float* ckpt, const void* dy,
             const float* dh_last, void* dx, void* dgr, void* dgi, float* dA, float* dh0, int64_t Bs, int64_t L,
             int64_t ED, int dtype, void* ws, hipStream_t st) {
-  const BwdPlan pl = bwd_plan(Bs, L, ED, dtype);
-  GlrArgs<T> a{};
-  a.x = static_cast<const T*>(x), a.gr = static_cast<const T*>(gr), a.gi = static_cast<const T*>(gi);
-  a.A = A, a.ckpt = const_cast<float*>(ckpt), a.dy = static_cast<const T*>(dy), a.dh_last = dh_last;
+  const int vec = vec_of(ED, dtype);
+  const Plan f = plan(Bs, L, ED, vec, bwd_waves(vec));
+  if (f.nchunks * f.ngroups > kMaxGrid) return SSM_ERR_DIM;
+  GlrArgs<T> a = glr_args<T>(x, gr, gi, A, Bs, L, ED, f, ws, st);
+  a.ckpt = const_cast<float*>(ckpt), a.dy = static_cast<const T*>(dy), a.dh_last = dh_last;
   a.dx = static_cast<T*>(dx), a.dgr = static_cast<T*>(dgr), a.dgi = static_cast<T*>(dgi), a.dh0 = dh0;
-  a.Bs = Bs, a.L = L, a.ED = ED, a.nchunks = pl.nchunks, a.steps = pl.steps, a.ckrows = pl.ckrows;
-  char* w = static_cast<char*>(ws);
-  a.agg = reinterpret_cast<float2*>(w);
-  a.enter = reinterpret_cast<float*>(w + glr_agg_bytes(pl, Bs * ED));
-  a.dA_part = reinterpret_cast<float*>(w + glr_agg_bytes(pl, Bs * ED) + glr_enter_bytes(pl, Bs * ED));
-  if constexpr (sizeof(T) == 2)
-    if (fwd_vec(ED, dtype) == 2) return launch_bwd<T, 2>(a, dA, st);
-  return launch_bwd<T, 1>(a, dA, st);
+  a.dA_part = reinterpret_cast<float*>(static_cast<char*>(ws) + f.bytes);
+  const dim3 grid(static_cast<unsigned>(f.nchunks * f.ngroups)), block(64 * bwd_waves(vec));
+  if constexpr (sizeof(T) == 2) {
+    if (vec == 2)
+      hipLaunchKernelGGL((glr_bwd_kernel<T, 2>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((glr_bwd_kernel<T, 1>), grid, block, 0, st, a);
+  } else {
+    hipLaunchKernelGGL((glr_bwd_kernel<T, 1>), grid, block, 0, st, a);
+  }
+  hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>((ED + 15) / 16)), dim3(1024), 0, st, a.dA_part, dA,
+                     Bs * f.nchunks, ED);
+  return hipGetLastError() == hipSuccess ? SSM_OK : SSM_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -746,14 +704,15 @@ extern "C" size_t ssm_glr_ckpt_bytes(int64_t Bs, int64_t L, int64_t ED) {
 extern "C" size_t ssm_glr_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype) {
   int64_t n, nck;
   if (glr_sizes(Bs, L, ED, dtype, &n, &nck) != SSM_OK || n == 0) return 0;
-  return static_cast<size_t>(fwd_plan(Bs, L, ED, dtype).bytes);
+  return static_cast<size_t>(plan(Bs, L, ED, vec_of(ED, dtype), kFwdWaves).bytes);
 }
 
 extern "C" size_t ssm_glr_bwd_workspace_bytes(int64_t Bs, int64_t L, int64_t ED, int dtype) {
   int64_t n, nck;
   if (glr_sizes(Bs, L, ED, dtype, &n, &nck) != SSM_OK || n == 0) return 0;
-  const BwdPlan pl = bwd_plan(Bs, L, ED, dtype);
-  return glr_agg_bytes(pl, Bs * ED) + 2 * glr_enter_bytes(pl, Bs * ED);
+  const int vec = vec_of(ED, dtype);
+  const Plan f = plan(Bs, L, ED, vec, bwd_waves(vec));
+  return static_cast<size_t>(f.bytes + Bs * f.nchunks * ED * 4);
 }
 
 extern "C" int ssm_glr_fwd(const void* x, const void* gr, const void* gi, const float* A, const float* h0, void* y,
