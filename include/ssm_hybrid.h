@@ -59,6 +59,10 @@ typedef struct {
  *               ED), for ssm_glr_bwd; ssm_glr_ckpt_bytes() bytes
  *   workspace : ssm_glr_workspace_bytes() bytes; no initialisation needed.
  *               NULL when that is zero
+ * Sequences of more than 128 steps (backward: 64 or 128) are split over
+ * workgroups that hand the state on and wait for each other, for a bounded
+ * time (SSM_SPLIT_SPIN_LIMIT in the environment: polls of a wait); one that
+ * gives up takes NaN for the state, so what follows from it is NaN.
  */
 #define SSM_GLR_CKPT_STEPS 16
 size_t ssm_glr_ckpt_bytes(int64_t Bs, int64_t L, int64_t ED);

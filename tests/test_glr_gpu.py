@@ -177,6 +177,27 @@ def test_repeated_calls_are_identical():
             assert torch.equal(v, first[k]), k
 
 
+@pytest.mark.parametrize("dtype", [f32, bf16])
+def test_waits_that_give_up_leave_nan(dtype, monkeypatch):
+    # with no polls allowed a wait holds only if the state is there at once; whatever
+    # a chunk that gave up leaves is NaN, everything else as without the limit
+    g = cuda(glr_inputs(2, 5000, 70, dtype, seed=12))
+    monkeypatch.delenv("SSM_SPLIT_SPIN_LIMIT", raising=False)
+    want = train(g)
+    monkeypatch.setenv("SSM_SPLIT_SPIN_LIMIT", "0")
+    got = train(g)
+    for name in ("y", "h_last"):
+        assert bool(((got[name] == want[name]) | got[name].isnan()).all()), name
+    # the backward alone, from a good forward's checkpoints
+    monkeypatch.delenv("SSM_SPLIT_SPIN_LIMIT")
+    ckpt = torch.empty(ssm.ssm_glr_ckpt_shape(2, 5000, 70), device="cuda")
+    ssm.ssm_glr_fwd(g["x"], g["gr"], g["gi"], g["A"], h0=g["h0"], ckpt=ckpt)
+    monkeypatch.setenv("SSM_SPLIT_SPIN_LIMIT", "0")
+    grads = ssm.ssm_glr_bwd(g["x"], g["gr"], g["gi"], g["A"], ckpt, g["dy"], dh_last=g["dh_last"], want_dh0=True)
+    for name, v in grads.items():
+        assert bool(((v == want[name]) | v.isnan()).all()), name
+
+
 def test_on_another_stream():
     t = glr_inputs(1, 1500, 64, f32, seed=14)
     g = cuda(t)
