@@ -281,12 +281,15 @@ __device__ __forceinline__ Mask mask_of(const SwaArgs<T>& p, int b) {
 // map deals the XCDs runs of kRun in turn (16384 tokens, window 2048, forward /
 // 2 x 4096, window 1024, training step: runs of 16 294 / 428 us, of 64 301 /
 // 406, a contiguous range for each XCD 298 / 409, which also leaves an XCD with
-// the short blocks at a sequence's start).
+// the short blocks at a sequence's start). Calls of fewer than 8 kRun get runs of
+// an eighth: the training step's dk and dv, 256 workgroups, then read 164 MB of
+// queries and not 623 (408 -> 398 us).
 constexpr int kRun = 64;
 __device__ __forceinline__ int xcd_order(int blk, int n) {
-  const int x = blk & 7, i = blk >> 3, whole = n / (8 * kRun) * (8 * kRun);
-  if (blk >= whole) return blk;
-  return ((i / kRun) * 8 + x) * kRun + i % kRun;
+  const int run = n >= 8 * kRun ? kRun : n / 8;
+  const int x = blk & 7, i = blk >> 3;
+  if (run == 0 || blk >= n / (8 * run) * (8 * run)) return blk;
+  return ((i / run) * 8 + x) * run + i % run;
 }
 
 // The key tiles (of KB keys) that positions [p0, p1] may see: those of the
