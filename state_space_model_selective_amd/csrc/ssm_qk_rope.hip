@@ -9,6 +9,9 @@
 // workgroup takes a few tokens and a slice of their heads: it forms the angles
 // once (64-bit reduction to a fraction of a turn, then float32) in LDS, for all
 // its heads, while its first loads are under way.
+//   Memory bounds it: 2x8192 tokens of 32 + 8 heads of 128, bf16, in 86 us (3.9
+// TB/s; the same accesses without the arithmetic take 76). Few tokens are a
+// chain of latencies: appending one to each of 64 rows takes 5.5 us.
 #include "hybrid_common.h"
 
 namespace {

