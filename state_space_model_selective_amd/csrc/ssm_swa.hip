@@ -670,15 +670,20 @@ __device__ __forceinline__ void dkdv_block(const SwaArgs<T>& p, int w, char* lds
               dp = mma(gf[kk], v[kk], dp);
             }
           }
-          Frag<T> qc[2][DB], gc[2][DB];
+          // (the operands of float32 at D = 128 are read as they are used: no
+          // registers are left to hold them)
+          constexpr bool AHEAD = D == 64 || sizeof(T) == 2;
+          Frag<T> qc[2][AHEAD ? DB : 1], gc[2][AHEAD ? DB : 1];
+          if constexpr (AHEAD) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-              gc[h][d] = QT::col(gs, r0 + 16 * h, d, lane);
-              qc[h][d] = QT::col(qs, r0 + 16 * h, d, lane);
-            }
-          in_order<T>();
+              for (int d = 0; d < DB; ++d) {
+                gc[h][d] = QT::col(gs, r0 + 16 * h, d, lane);
+                qc[h][d] = QT::col(qs, r0 + 16 * h, d, lane);
+              }
+            in_order<T>();
+          }
           // (keys on the other side of S are other columns: they are formed and not stored)
           const bool full = m.all(pb0, pb1, j0, j0 + 31) && ib + 31 < p.Lq;
 #pragma unroll
@@ -707,8 +712,14 @@ __device__ __forceinline__ void dkdv_block(const SwaArgs<T>& p, int w, char* lds
             const Frag<T> wt = as_operand<T>(s, h), ds = as_operand<T>(dp, h);
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
-              dv[d] = mma(gc[h][d], wt, dv[d]);
-              dk[d] = mma(qc[h][d], ds, dk[d]);
+              if constexpr (AHEAD) {
+                dv[d] = mma(gc[h][d], wt, dv[d]);
+                dk[d] = mma(qc[h][d], ds, dk[d]);
+              } else {
+                dv[d] = mma(QT::col(gs, r0 + 16 * h, d, lane), wt, dv[d]);
+                dk[d] = mma(QT::col(qs, r0 + 16 * h, d, lane), ds, dk[d]);
+                __builtin_amdgcn_sched_barrier(0);
+              }
             }
           }
         }
