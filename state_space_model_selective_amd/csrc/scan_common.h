@@ -7,7 +7,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <cstdlib>
 
 // Internal linkage: each translation unit gets its own copy.
 namespace {
@@ -232,19 +231,6 @@ size_t spread_lds(int64_t nblk, size_t lds_static, int max_per_cu) {
   total = (total + 511) & ~static_cast<size_t>(511);
   if (total > static_cast<size_t>(lds_cu / want) || total <= lds_static) return 0;
   return total - lds_static;
-}
-
-// Iterations of a hand-off wait before it gives up (s_sleep 4 each: about
-// 7 s at 2^26). SSM_SPLIT_SPIN_LIMIT in the environment overrides it, so
-// that a test can force the give-up path from the host.
-[[maybe_unused]] unsigned split_spin_limit() {
-  const char* e = std::getenv("SSM_SPLIT_SPIN_LIMIT");
-  if (e && *e) {
-    char* end = nullptr;
-    const unsigned long v = std::strtoul(e, &end, 10);
-    if (end && *end == '\0') return static_cast<unsigned>(std::min<unsigned long>(v, 1ul << 26));
-  }
-  return 1u << 26;
 }
 
 // Clears the split-sequence workspace header and flags (a kernel rather than

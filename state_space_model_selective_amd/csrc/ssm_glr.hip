@@ -10,6 +10,7 @@
 // Handoff); then every step's state follows from the one entering the wave.
 // Backward: the same against time with the maps of the adjoint, states starting
 // from the forward's checkpoints every 16 steps.
+#include <cstdlib>
 #include <type_traits>
 
 #include "hybrid_common.h"
@@ -598,6 +599,18 @@ __global__ __launch_bounds__(256) void glr_step_kernel(const T* x, const T* gr, 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+// Polls of a hand-off wait before it gives up (the forward scan's limit and
+// its override from the environment, by which a test forces the give-up path).
+unsigned spin_limit() {
+  const char* e = std::getenv("SSM_SPLIT_SPIN_LIMIT");
+  if (e && *e) {
+    char* end = nullptr;
+    const unsigned long v = std::strtoul(e, &end, 10);
+    if (end && *end == '\0') return static_cast<unsigned>(std::min<unsigned long>(v, 1ul << 26));
+  }
+  return 1u << 26;
+}
+
 // VEC: 4 bytes a lane (256 a wave and row), or single channels where a pair
 // would straddle the row's end.
 int vec_of(int64_t ED, int dtype) { return dtype == SSM_BF16 && ED % 2 == 0 ? 2 : 1; }
@@ -645,7 +658,7 @@ GlrArgs<T> glr_args(const void* x, const void* gr, const void* gi, const float* 
     char* w = static_cast<char*>(ws);
     a.hdr = reinterpret_cast<unsigned*>(w), a.flag = reinterpret_cast<unsigned*>(w + f.flag);
     a.state = reinterpret_cast<uint64_t*>(w + f.state), a.map = reinterpret_cast<uint64_t*>(w + f.map);
-    a.spin_limit = split_spin_limit();
+    a.spin_limit = spin_limit();
     hipLaunchKernelGGL(zero_words_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((f.map / 4 + 255) / 256, 1024))),
                        dim3(256), 0, st, static_cast<unsigned*>(ws), f.map / 4);
   }

@@ -982,6 +982,19 @@ struct SplitPlan {
   size_t flag_off, state_off, sd_off, gstate_off, bytes;
 };
 
+// Iterations of a hand-off wait before it gives up (s_sleep 4 each: about
+// 7 s at 2^26). SSM_SPLIT_SPIN_LIMIT in the environment overrides it, so
+// that a test can force the give-up path from the host.
+unsigned split_spin_limit() {
+  const char* e = std::getenv("SSM_SPLIT_SPIN_LIMIT");
+  if (e && *e) {
+    char* end = nullptr;
+    const unsigned long v = std::strtoul(e, &end, 10);
+    if (end && *end == '\0') return static_cast<unsigned>(std::min<unsigned long>(v, 1ul << 26));
+  }
+  return 1u << 26;
+}
+
 SplitPlan plan_split(int64_t Bs, int64_t L, int64_t ED, int bidir, int ncu) {
   SplitPlan sp{};
   sp.nbg = Bs * ((ED + 15) / 16);
